@@ -14,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -34,7 +36,7 @@ def _nvcc() -> str:
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + glob.glob(os.path.join(INCLUDE, "*.h")))
+                  + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def needs_build(path: str = LIB_PATH) -> bool:
@@ -44,26 +46,39 @@ def needs_build(path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(s) > t for s in _sources())
 
 
+def _run(cmd):
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    return cmd, proc.returncode, proc.stdout + proc.stderr
+
+
+def _run_all(results, verbose: bool) -> None:
+    for cmd, code, text in results:
+        if code != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + text)
+        if verbose:
+            sys.stdout.write(text)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False, out: str | None = None) -> str:
     """Compile the library; returns its path.  ``debug`` adds -DFA_DEBUG and,
     unless ``out`` names another file, writes libfa_b200_debug.so."""
     path = out or (DEBUG_LIB_PATH if debug else LIB_PATH)
     if not force and not needs_build(path):
         return path
-    cmd = [
-        _nvcc(), *ARCH_FLAGS, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-        "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
-        "-o", path + ".tmp", os.path.join(CSRC, "fa_api.cu"),
-    ]
+    flags = [*ARCH_FLAGS, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
+             "-I", INCLUDE, "-I", CSRC]
     if debug:
-        cmd.insert(1, "-DFA_DEBUG")
+        flags.append("-DFA_DEBUG")
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    proc = subprocess.run(cmd, capture_output=True, text=True)
-    if proc.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + proc.stdout + proc.stderr)
-    if verbose:
-        sys.stdout.write(proc.stdout + proc.stderr)
+        flags.append("-Xptxas=-v")
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    with tempfile.TemporaryDirectory() as tmp:
+        # one compiler process for each translation unit, then one link
+        objs = [os.path.join(tmp, os.path.basename(u) + ".o") for u in units]
+        cmds = [[_nvcc(), *flags, "-c", u, "-o", o] for u, o in zip(units, objs)]
+        with ThreadPoolExecutor(len(cmds)) as pool:
+            _run_all(pool.map(_run, cmds), verbose)
+        _run_all([_run([_nvcc(), *ARCH_FLAGS, "-shared", "-o", path + ".tmp", *objs])], verbose)
     os.replace(path + ".tmp", path)
     return path
 

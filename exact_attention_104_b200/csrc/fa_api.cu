@@ -16,6 +16,7 @@
 #include "fa_fwd.cuh"
 #include "fa_fwd_pair.cuh"
 #include "fa_fwd_persistent.cuh"
+#include "fa_host.h"
 #include "fa_varlen.cuh"
 
 // Scratch of fa_bwd_noalloc: a fixed device array instead of a caller buffer.
@@ -23,84 +24,9 @@
 // stand-in, not device memory); noalloc_scratch() resolves its device address.
 static __device__ __align__(256) unsigned char g_fa_noalloc_scratch[FA_NOALLOC_SCRATCH_BYTES];
 
-namespace {
+using namespace fa_host;
 
-constexpr int kMaxDevices = 64;
-std::atomic<long long> g_wait_cap{1LL << 31};  // may be set from any host thread
-
-// pending one-shot profiling events of this host thread (fa_profile_next)
-thread_local cudaEvent_t t_prof_start = nullptr;
-thread_local cudaEvent_t t_prof_stop = nullptr;
-
-struct ProfileScope {
-  cudaEvent_t start, stop;
-  cudaStream_t stream;
-  explicit ProfileScope(cudaStream_t s) : start(t_prof_start), stop(t_prof_stop), stream(s) {
-    t_prof_start = t_prof_stop = nullptr;
-    if (start) cudaEventRecord(start, stream);
-  }
-  ~ProfileScope() {
-    if (stop) cudaEventRecord(stop, stream);
-  }
-};
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
-// 2-D view [rows, d] of a bf16 tensor; boxes of 64 columns (128 bytes, the
-// swizzle span) by `box_rows` rows, 128-byte swizzled in shared memory.
-bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, int d, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D view [rows, d] of an fp32 tensor, unswizzled boxes of box_cols x box_rows
-// (used as the destination of TMA reduce-adds).
-bool make_map_f32(CUtensorMap* m, const void* ptr, uint64_t rows, int d, int box_cols, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 4};
-  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct DeviceInfo {
-  bool checked = false;
-  bool sm100 = false;
-  int sms = 0;
-  int* err = nullptr;
-};
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mu;
-
-// Checks for an sm_100 device and resolves the error word's device address
-// (once per device, with that device current).
-fa_status current_device(DeviceInfo** out) {
+fa_status fa_host::current_device(DeviceInfo** out) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
@@ -128,19 +54,7 @@ fa_status current_device(DeviceInfo** out) {
   return FA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range span(const void* p, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// N rounded up to a whole number of 128-row tiles.
-long long pad128(long long n) { return (n + 127) / 128 * 128; }
+namespace {
 
 // Size checks shared by both passes.  Returns FA_OK, or the status to report;
 // sets *empty for a problem with nothing to compute.
@@ -158,8 +72,6 @@ fa_status check_sizes(int B, int Hq, int Hkv, int N, int d, float scale, bool* e
   if ((long long)B * Hq * pad128(N) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
-
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // The per-warpgroup register split (setmaxnreg) of a kernel is only valid for
 // a launch allocation inside [C::MIN_LAUNCH_REGS, C::MAX_LAUNCH_REGS]: below
