@@ -24,6 +24,17 @@ from .binding import (  # noqa: F401
     fa_bwd_varlen_workspace_bytes,
     fa_fwd_decode,
     fa_decode_workspace_bytes,
+    attention_decode_prefix,
+    attention_decode_weights,
+    attention_key_weights,
+    cache_evict,
+    fa_fwd_decode_prefix,
+    fa_decode_prefix_workspace_bytes,
+    fa_fwd_decode_weights,
+    fa_decode_weights_workspace_bytes,
+    fa_key_weights,
+    fa_key_weights_workspace_bytes,
+    fa_cache_evict,
     lib,
     LIB_PATH,
 )

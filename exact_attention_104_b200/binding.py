@@ -7,6 +7,7 @@ library is missing or the device is unsupported, calls raise ``FAError``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -73,6 +74,20 @@ def lib() -> ctypes.CDLL:
     L.fa_fwd_varlen.restype = i
     L.fa_bwd_varlen.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, z, vp]
     L.fa_bwd_varlen.restype = i
+    L.fa_decode_prefix_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    L.fa_decode_prefix_workspace_bytes.restype = z
+    L.fa_fwd_decode_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, z, vp]
+    L.fa_fwd_decode_prefix.restype = i
+    L.fa_decode_weights_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.fa_decode_weights_workspace_bytes.restype = z
+    L.fa_fwd_decode_weights.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, z, vp]
+    L.fa_fwd_decode_weights.restype = i
+    L.fa_key_weights_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    L.fa_key_weights_workspace_bytes.restype = z
+    L.fa_key_weights.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, z, vp]
+    L.fa_key_weights.restype = i
+    L.fa_cache_evict.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp]
+    L.fa_cache_evict.restype = i
     _lib = L
     return L
 
@@ -189,6 +204,54 @@ def fa_bwd_varlen(q, k, v, o, lse, do, dq, dk, dv, cu_seqlens, nseq, Hq, Hkv, T,
     return lib().fa_bwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq), _ptr(dk),
                                _ptr(dv), _ptr(cu_seqlens), nseq, Hq, Hkv, T, max_seqlen, d, int(bool(causal)),
                                float(scale), _ptr(workspace), int(workspace_bytes), _stream_handle(stream))
+
+
+def fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d) -> int:
+    return int(lib().fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d))
+
+
+def fa_fwd_decode_prefix(q, k_prefix, v_prefix, k, v, lengths, o, lse, B, Hq, Hkv, Nq, Np, Ncap, d, causal, scale,
+                         workspace, workspace_bytes, stream=None) -> int:
+    """Raw C-ABI call of decoding for a batch that shares a prefix.  Returns
+    the status."""
+    return lib().fa_fwd_decode_prefix(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(lengths),
+                                      _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Np, Ncap, d, int(bool(causal)),
+                                      float(scale), _ptr(workspace), int(workspace_bytes), _stream_handle(stream))
+
+
+def fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d) -> int:
+    return int(lib().fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+
+
+def fa_fwd_decode_weights(q, k, v, lengths, weights, weights_out, o, lse, B, Hq, Hkv, Nq, Nk, d, causal, scale,
+                          workspace, workspace_bytes, stream=None) -> int:
+    """Raw C-ABI call of decoding that adds up every key's attention weight.
+    Returns the status."""
+    return lib().fa_fwd_decode_weights(_ptr(q), _ptr(k), _ptr(v), _ptr(lengths), _ptr(weights), _ptr(weights_out),
+                                       _ptr(o), _ptr(lse), B, Hq, Hkv, Nq, Nk, d, int(bool(causal)), float(scale),
+                                       _ptr(workspace), int(workspace_bytes), _stream_handle(stream))
+
+
+def fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d) -> int:
+    return int(lib().fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+
+
+def fa_key_weights(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale, workspace,
+                   workspace_bytes, stream=None) -> int:
+    """Raw C-ABI call of the keys' attention weights from queries whose LSE is
+    known.  Returns the status."""
+    return lib().fa_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(lengths), _ptr(weights), _ptr(weights_out), B, Hq,
+                                Hkv, Nq, Nk, d, int(bool(causal)), float(scale), _ptr(workspace),
+                                int(workspace_bytes), _stream_handle(stream))
+
+
+def fa_cache_evict(k, v, weights, lengths, k_out, v_out, weights_out, index, lengths_out, B, Hkv, Nk, out_cap, budget,
+                   recent, d, stream=None) -> int:
+    """Raw C-ABI call of the eviction by accumulated weight.  Returns the
+    status."""
+    return lib().fa_cache_evict(_ptr(k), _ptr(v), _ptr(weights), _ptr(lengths), _ptr(k_out), _ptr(v_out),
+                                _ptr(weights_out), _ptr(index), _ptr(lengths_out), B, Hkv, Nk, out_cap, budget,
+                                recent, d, _stream_handle(stream))
 
 
 def fa_profile_next(start_event=None, stop_event=None) -> int:
@@ -320,3 +383,171 @@ def attention_backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causa
     _check(fa_bwd_varlen(q, k, v, o, lse, do, dq, dk, dv, cu_seqlens, nseq, Hq, Hkv, T, max_seqlen, d, causal,
                          scale, workspace, workspace.numel() * workspace.element_size(), stream), "fa_bwd_varlen")
     return dq, dk, dv
+
+
+# ------------------------------------------------------- bounded key/value caches
+class _CacheCall:
+    """Argument checks and placement of one cache call: every tensor lies on the
+    device of the first, the call runs with that device current, and on
+    ``stream`` (or that device's current stream), from whose memory pool the
+    tensors it allocates come."""
+
+    def __init__(self, where, first, stream):
+        self.where = where
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            self.refuse("inputs must be CUDA tensors")
+        self.device = first.device
+        # tensors of a stream given as a handle belong to that stream's pool too
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream)
+                      else torch.cuda.default_stream(self.device))
+        if stream is not None:
+            if stream.device != self.device:
+                self.refuse("the stream belongs to another device")
+            self.scope = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != self.device.index:
+            self.scope = torch.cuda.device(self.device)
+        else:
+            self.scope = contextlib.nullcontext()
+
+    def refuse(self, why):
+        raise FAError(FA_ERR_INVALID_ARG, f"{self.where}: {why}")
+
+    def check(self, name, t, shape, dtype):
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            self.refuse(f"{name} must be a tensor on {self.device}")
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            self.refuse(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+    def given_or_new(self, name, t, shape, dtype):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        self.check(name, t, shape, dtype)
+        return t
+
+    def scratch(self, t, need):
+        """The caller's workspace, or a new one of the size needed."""
+        if t is None:
+            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        if not isinstance(t, torch.Tensor) or t.device != self.device or not t.is_contiguous():
+            self.refuse(f"workspace must be a contiguous tensor on {self.device}")
+        return t
+
+
+def _cache_dims(call, q, k):
+    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        call.refuse("q and k must be [B, H, N, d]")
+    return (*q.shape, k.shape[1], k.shape[2])
+
+
+def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lengths=None, causal=False, scale=None, out=None, lse=None,
+                            workspace=None, stream=None):
+    """O, LSE of Nq queries q [B,Hq,Nq,d] in a batch that shares a prefix: the
+    keys of sequence b are k_prefix [Hkv,Np,d] followed by the first lengths[b]
+    rows of k[b] ([B,Hkv,Ncap,d]; lengths None: all of them); the queries are
+    its last Nq positions (see fa_fwd_decode_prefix).  Np and Ncap may be 0.
+    Returns (o bf16 [B,Hq,Nq,d], lse fp32 [B,Hq,Nq])."""
+    call = _CacheCall("attention_decode_prefix", q, stream)
+    B, Hq, Nq, d, Hkv, Ncap = _cache_dims(call, q, k)
+    if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
+        call.refuse("k_prefix must be [Hkv, Np, d]")
+    Np = k_prefix.shape[1]
+    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    for name, t in (("k", k), ("v", v)):
+        call.check(name, t, (B, Hkv, Ncap, d), torch.bfloat16)
+    for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
+        call.check(name, t, (Hkv, Np, d), torch.bfloat16)
+    if lengths is not None:
+        call.check("lengths", lengths, (B,), torch.int32)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with call.scope:
+        out = call.given_or_new("out", out, (B, Hq, Nq, d), torch.bfloat16)
+        lse = call.given_or_new("lse", lse, (B, Hq, Nq), torch.float32)
+        workspace = call.scratch(workspace, fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d))
+        _check(fa_fwd_decode_prefix(q, k_prefix, v_prefix, k, v, lengths, out, lse, B, Hq, Hkv, Nq, Np, Ncap, d,
+                                    causal, scale, workspace, workspace.numel() * workspace.element_size()),
+               "fa_fwd_decode_prefix")
+    return out, lse
+
+
+def attention_decode_weights(q, k, v, weights=None, lengths=None, causal=False, scale=None, out=None, lse=None,
+                             weights_out=None, workspace=None, stream=None):
+    """O, LSE of Nq queries q [B,Hq,Nq,d] against the first lengths[b] rows of
+    the caches k, v [B,Hkv,Nk,d], and the attention weight that every key
+    received, added to weights (fp32 [B,Hkv,Nk]; None: zero).  Passing the same
+    tensor as weights and weights_out updates it in place (see
+    fa_fwd_decode_weights).  Returns (o, lse, weights_out)."""
+    call = _CacheCall("attention_decode_weights", q, stream)
+    B, Hq, Nq, d, Hkv, Nk = _cache_dims(call, q, k)
+    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    for name, t in (("k", k), ("v", v)):
+        call.check(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    if weights is not None:
+        call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+    if lengths is not None:
+        call.check("lengths", lengths, (B,), torch.int32)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with call.scope:
+        out = call.given_or_new("out", out, (B, Hq, Nq, d), torch.bfloat16)
+        lse = call.given_or_new("lse", lse, (B, Hq, Nq), torch.float32)
+        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
+        workspace = call.scratch(workspace, fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        _check(fa_fwd_decode_weights(q, k, v, lengths, weights, weights_out, out, lse, B, Hq, Hkv, Nq, Nk, d, causal,
+                                     scale, workspace, workspace.numel() * workspace.element_size()),
+               "fa_fwd_decode_weights")
+    return out, lse, weights_out
+
+
+def attention_key_weights(q, k, lse, weights=None, lengths=None, causal=False, scale=None, weights_out=None,
+                          workspace=None, stream=None):
+    """The attention weight that every key of the caches k [B,Hkv,Nk,d] receives
+    from the queries q [B,Hq,Nq,d] (the last Nq positions of each sequence)
+    whose lse [B,Hq,Nq] is known, added to weights (fp32 [B,Hkv,Nk]; None:
+    zero); see fa_key_weights.  Returns weights_out."""
+    call = _CacheCall("attention_key_weights", q, stream)
+    B, Hq, Nq, d, Hkv, Nk = _cache_dims(call, q, k)
+    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    call.check("k", k, (B, Hkv, Nk, d), torch.bfloat16)
+    call.check("lse", lse, (B, Hq, Nq), torch.float32)
+    if weights is not None:
+        call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+    if lengths is not None:
+        call.check("lengths", lengths, (B,), torch.int32)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with call.scope:
+        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
+        workspace = call.scratch(workspace, fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        _check(fa_key_weights(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale,
+                              workspace, workspace.numel() * workspace.element_size()), "fa_key_weights")
+    return weights_out
+
+
+def cache_evict(k, v, weights, budget, recent=0, lengths=None, out_cap=None, k_out=None, v_out=None, weights_out=None,
+                index=None, lengths_out=None, stream=None):
+    """Cuts the caches k, v [B,Hkv,Nk,d] with the accumulated weights fp32
+    [B,Hkv,Nk] down to budget keys a kv head: the last ``recent`` ones and, of
+    the others, those of greatest weight, in their order (see fa_cache_evict).
+    The outputs have out_cap slots (None: budget; more leaves room to decode
+    into, and is not written).  Returns (k_out, v_out, weights_out, index int32
+    [B,Hkv,out_cap], lengths_out int32 [B])."""
+    call = _CacheCall("cache_evict", k, stream)
+    if k.dim() != 4:
+        call.refuse("k must be [B, Hkv, Nk, d]")
+    B, Hkv, Nk, d = k.shape
+    for name, t in (("k", k), ("v", v)):
+        call.check(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+    if lengths is not None:
+        call.check("lengths", lengths, (B,), torch.int32)
+    out_cap = budget if out_cap is None else out_cap
+    if not 1 <= budget <= out_cap or not 0 <= recent <= budget:
+        call.refuse("budget must be in 1 .. out_cap and recent in 0 .. budget")
+    with call.scope:
+        k_out = call.given_or_new("k_out", k_out, (B, Hkv, out_cap, d), torch.bfloat16)
+        v_out = call.given_or_new("v_out", v_out, (B, Hkv, out_cap, d), torch.bfloat16)
+        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, out_cap), torch.float32)
+        index = call.given_or_new("index", index, (B, Hkv, out_cap), torch.int32)
+        lengths_out = call.given_or_new("lengths_out", lengths_out, (B,), torch.int32)
+        _check(fa_cache_evict(k, v, weights, lengths, k_out, v_out, weights_out, index, lengths_out, B, Hkv, Nk,
+                              out_cap, budget, recent, d), "fa_cache_evict")
+    return k_out, v_out, weights_out, index, lengths_out

@@ -713,6 +713,15 @@ fa_status fa_device_status(void* stream) {
   if (cudaMemcpy(&host, di->err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return FA_ERR_CUDA;
   if (host != 0 && cudaMemcpy(di->err, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
     return FA_ERR_CUDA;
+#ifdef FA_DEBUG
+  int* word = nullptr;
+  int check = 0;
+  if (cache_check_word(&word) != cudaSuccess ||
+      cudaMemcpy(&check, word, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
+    return FA_ERR_CUDA;
+  if (check != 0) host = check;
+#endif
   if (host == 0) return FA_OK;
   if ((host & 0xff) == fa::kDevCheck) return FA_ERR_DEVICE_CHECK;
   if ((host & 0xff) == fa::kDevBadSeqlens) return FA_ERR_INVALID_ARG;

@@ -1,0 +1,413 @@
+// Host side of the cache operators: decoding for a batch that shares a prefix,
+// decoding that accumulates the keys' attention weights, the same weights from
+// a prompt's queries, and eviction by them.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_cache_attn.cuh"
+#include "fa_evict.cuh"
+#include "fa_host.h"
+#include "fa_key_weights.cuh"
+
+using namespace fa_host;
+
+cudaError_t fa_host::cache_check_word(int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_fa_err);
+}
+
+namespace {
+
+constexpr long long kIndexLimit = (1LL << 31) - 4096;  // row coordinates, with room for a box past the end
+
+// Allows `kern` its dynamic shared memory, once per device.
+template <class Kern>
+fa_status allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  const unsigned long long bit = 1ULL << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return FA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  done.fetch_or(bit, std::memory_order_release);
+  return FA_OK;
+}
+
+fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// No output may overlap an input or another output.
+template <int NI, int NO>
+bool disjoint(const Range (&ins)[NI], const Range (&outs)[NO]) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < NI; ++j)
+      if (overlap(outs[i], ins[j])) return false;
+    for (int j = i + 1; j < NO; ++j)
+      if (overlap(outs[i], outs[j])) return false;
+  }
+  return true;
+}
+
+fa_status cache_sizes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, float scale, bool* empty) {
+  *empty = false;
+  if (B < 0 || Nq < 0 || Np < 0 || Ncap < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FA_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (Nq > 256) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Nq == 0) *empty = true;
+  if (B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hq * Nq > kIndexLimit || (long long)B * Hkv * Ncap > kIndexLimit ||
+      (long long)Hkv * Np > kIndexLimit || (long long)Np + Ncap > kIndexLimit)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// How the keys are cut into runs: a pure function of the sizes, so that the
+// workspace sizes need no device.  Runs of equal length for the prefix and the
+// own keys, as many as give about kCacheCtas CTAs in all, but of 128 keys at
+// least (one step of each of a CTA's four warps).
+constexpr int kCacheCtas = 592;
+struct CachePlan {
+  int rg_p = 0, n_split_p = 0, kps_p = 128, rg_o = 0, n_split_o = 0, kps_o = 128;
+  size_t part_o_bytes = 0, part_ml_bytes = 0, score_bytes = 0;
+  size_t total() const { return part_o_bytes + part_ml_bytes + score_bytes; }
+};
+
+CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bool scores) {
+  CachePlan pl;
+  const long long R = (long long)(Hq / Hkv) * Nq, M = B * R;
+  pl.rg_p = (int)((M + 15) / 16);
+  pl.rg_o = (int)((R + 15) / 16);
+  const long long work = (long long)Hkv * pl.rg_p * Np + (long long)B * Hkv * pl.rg_o * Ncap;
+  const long long kps = std::max<long long>(128, ((work + kCacheCtas - 1) / kCacheCtas + 127) / 128 * 128);
+  pl.kps_p = pl.kps_o = (int)std::min<long long>(kps, 1LL << 30);
+  pl.n_split_p = (int)((Np + (long long)pl.kps_p - 1) / pl.kps_p);
+  pl.n_split_o = (int)((Ncap + (long long)pl.kps_o - 1) / pl.kps_o);
+  const size_t rows = (size_t)pl.n_split_p * Hkv * M + (size_t)pl.n_split_o * B * Hkv * R;
+  pl.part_o_bytes = round256(rows * d * 4);
+  pl.part_ml_bytes = round256(rows * 2 * 4);
+  if (scores) pl.score_bytes = round256((size_t)B * Hkv * R * ((Ncap + 31) / 32 * 32) * 4);
+  return pl;
+}
+
+template <int D>
+fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, cudaStream_t s) {
+  using C = fa::CacheCfg<D>;
+  auto kern = fa::fa_cache_split_kernel<D>;
+  static std::atomic<unsigned long long> allowed{0};
+  const fa_status st = allow_smem(kern, C::SMEM_BYTES, allowed);
+  if (st != FA_OK) return st;
+  const long long ctas = (long long)p.Hkv * p.rg_p * p.n_split_p + (long long)p.B * p.Hkv * p.rg_o * p.n_split_o;
+  if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  if (ctas > 0) {
+    kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p);
+    if (launched() != FA_OK) return FA_ERR_CUDA;
+  }
+  const long long rows = (long long)p.B * p.Hq * p.Nq;
+  if (rows > 0) {
+    fa::fa_cache_combine_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+    if (launched() != FA_OK) return FA_ERR_CUDA;
+  }
+  if (p.weights_out && p.Ncap > 0) {
+    fa::fa_cache_weights_kernel<<<dim3((unsigned)((p.Ncap + 1023) / 1024), (unsigned)(p.B * p.Hkv)), 256, 0, s>>>(p);
+    return launched();
+  }
+  return FA_OK;
+}
+
+// Shared by the two decoding calls; weights_out null for the prefix form.
+fa_status cache_decode(const void* q, const void* kp, const void* vp, const void* k, const void* v,
+                       const int* lengths, const float* weights, float* weights_out, void* o, float* lse, int B,
+                       int Hq, int Hkv, int Nq, int Np, int Ncap, int d, int causal, float scale, void* workspace,
+                       size_t workspace_bytes, cudaStream_t s) {
+  const bool scores = weights_out != nullptr;
+  const CachePlan pl = cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, scores);
+  if (!workspace || (Nq > 0 && (!q || !o || !lse || (Np > 0 && (!kp || !vp)) || (Ncap > 0 && (!k || !v)))))
+    return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, kp, vp, k, v, (const void*)o, (const void*)lse})
+    if (!aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned4(lengths) || !aligned4(weights) || !aligned4(weights_out)) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.total()) return FA_ERR_INVALID_ARG;
+  const size_t qbytes = (size_t)B * Hq * Nq * d * 2, lbytes = (size_t)B * Hq * Nq * 4;
+  const size_t kvbytes = (size_t)B * Hkv * Ncap * d * 2, pbytes = (size_t)Hkv * Np * d * 2;
+  const size_t wbytes = (size_t)B * Hkv * Ncap * 4;
+  // weights_out may be weights itself
+  const Range ins[7] = {span(q, qbytes),
+                        span(kp, pbytes),
+                        span(vp, pbytes),
+                        span(k, kvbytes),
+                        span(v, kvbytes),
+                        span(lengths, lengths ? (size_t)B * 4 : 0),
+                        span(weights, weights && weights != weights_out ? wbytes : 0)};
+  const Range outs[4] = {span(o, qbytes), span(lse, lbytes), span(workspace, pl.total()),
+                         span(weights_out, weights_out ? wbytes : 0)};
+  if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  const fa_status st = current_device(&di);
+  if (st != FA_OK) return st;
+
+  // an absent cache's maps are never read: the other's stand in
+  const int box = d == 256 ? fa::CacheCfg<256>::CH : fa::CacheCfg<128>::CH;
+  CUtensorMap maps[4] = {};
+  const uint64_t prows = (uint64_t)Hkv * Np, krows = (uint64_t)B * Hkv * Ncap;
+  if (Np > 0 && (!make_map(&maps[0], kp, prows, d, box) || !make_map(&maps[1], vp, prows, d, box))) return FA_ERR_CUDA;
+  if (Nq > 0 && Ncap > 0 && (!make_map(&maps[2], k, krows, d, box) || !make_map(&maps[3], v, krows, d, box))) return FA_ERR_CUDA;
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fa::CacheParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.lengths = lengths;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + pl.part_o_bytes);
+  p.scores = scores ? reinterpret_cast<float*>(ws + pl.part_o_bytes + pl.part_ml_bytes) : nullptr;
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Nq = Nq;
+  p.R = p.G * Nq;
+  p.M = B * p.R;
+  p.Np = Np;
+  p.Ncap = Ncap;
+  p.cap_pad = (Ncap + 31) / 32 * 32;
+  p.rg_p = pl.rg_p;
+  p.n_split_p = pl.n_split_p;
+  p.kps_p = pl.kps_p;
+  p.rg_o = pl.rg_o;
+  p.n_split_o = pl.n_split_o;
+  p.kps_o = pl.kps_o;
+  p.causal = causal != 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
+  p.err = di->err;
+  switch (d) {
+    case 64: return launch_cache<64>(maps, p, s);
+    case 128: return launch_cache<128>(maps, p, s);
+    default: return launch_cache<256>(maps, p, s);
+  }
+}
+
+// ------------------------------------------------------------ key weights
+fa_status key_weights_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, bool* empty) {
+  *empty = false;
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FA_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Nk == 0) {
+    *empty = true;
+    return FA_OK;
+  }
+  if (B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
+  if (Nq > 0 && (long long)B * Hq > kIndexLimit / Nq) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > 65535 || (long long)B * Hkv * pad128(Nk) > kIndexLimit) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// Steps (head, 128 query rows) of a key tile are cut into runs of at least 8
+// where the key tiles alone give fewer than about two CTAs an SM.
+struct KeyWPlan {
+  int key_tiles, q_tiles, n_run, steps_per_run;
+  size_t part_bytes;
+};
+KeyWPlan key_weights_plan(int B, int Hq, int Hkv, int Nq, int Nk) {
+  KeyWPlan pl;
+  pl.key_tiles = (Nk + 127) / 128;
+  pl.q_tiles = (Nq + 127) / 128;
+  const long long steps = std::max<long long>(1, (long long)(Hq / Hkv) * pl.q_tiles);
+  const long long units = (long long)B * Hkv * pl.key_tiles;
+  const long long want = std::max<long long>(1, (2 * 148 + units - 1) / units);
+  const long long spr = std::max<long long>(std::min<long long>(8, steps), (steps + want - 1) / want);
+  pl.steps_per_run = (int)std::min<long long>(spr, 1LL << 30);
+  pl.n_run = (int)((steps + pl.steps_per_run - 1) / pl.steps_per_run);
+  pl.part_bytes = pl.n_run > 1 ? round256((size_t)pl.n_run * B * Hkv * pl.key_tiles * 128 * 4) : 0;
+  return pl;
+}
+
+template <int D>
+fa_status launch_key_weights(const CUtensorMap& tq, const CUtensorMap& tk, const fa::KeyWParams& p, cudaStream_t s) {
+  using C = fa::KeyWCfg<D>;
+  auto kern = fa::fa_key_weights_kernel<D>;
+  static std::atomic<unsigned long long> allowed{0};
+  const fa_status st = allow_smem(kern, C::SMEM_BYTES, allowed);
+  if (st != FA_OK) return st;
+  const long long ctas = (long long)p.B * p.Hkv * p.key_tiles * p.n_run;
+  if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, s>>>(tq, tk, p);
+  if (launched() != FA_OK) return FA_ERR_CUDA;
+  if (p.n_run > 1) {
+    fa::fa_key_weights_reduce_kernel<<<dim3((unsigned)((p.Ncap + 255) / 256), (unsigned)(p.B * p.Hkv)), 256, 0, s>>>(p);
+    return launched();
+  }
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d) {
+  bool empty = false;
+  if (cache_sizes(B, Hq, Hkv, Nq, Np, Ncap, d, 1.f, &empty) != FA_OK) return 0;
+  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, false).total());
+}
+
+fa_status fa_fwd_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                               const void* v, const int* lengths, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                               int Np, int Ncap, int d, int causal, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  bool empty = false;
+  const fa_status st = cache_sizes(B, Hq, Hkv, Nq, Np, Ncap, d, scale, &empty);
+  if (st != FA_OK || empty) return st;
+  return cache_decode(q, k_prefix, v_prefix, k, v, lengths, nullptr, nullptr, o, lse, B, Hq, Hkv, Nq, Np, Ncap, d,
+                      causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  bool empty = false;
+  if (cache_sizes(B, Hq, Hkv, Nq, 0, Nk, d, 1.f, &empty) != FA_OK) return 0;
+  if ((long long)B * Hkv > 65535) return 0;
+  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, 0, Nk, d, true).total());
+}
+
+fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, const int* lengths, const float* weights,
+                                float* weights_out, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  bool empty = false;
+  const fa_status st = cache_sizes(B, Hq, Hkv, Nq, 0, Nk, d, scale, &empty);
+  if (st != FA_OK || B == 0 || (Nq == 0 && Nk == 0)) return st;
+  if ((long long)B * Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (Nk > 0 && !weights_out) return FA_ERR_INVALID_ARG;
+  return cache_decode(q, nullptr, nullptr, k, v, lengths, weights, weights_out, o, lse, B, Hq, Hkv, Nq, 0, Nk, d,
+                      causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  bool empty = false;
+  if (key_weights_sizes(B, Hq, Hkv, Nq, Nk, d, 1.f, &empty) != FA_OK) return 0;
+  return empty ? 256 : std::max<size_t>(256, key_weights_plan(B, Hq, Hkv, Nq, Nk).part_bytes);
+}
+
+fa_status fa_key_weights(const void* q, const void* k, const float* lse, const int* lengths, const float* weights,
+                         float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  bool empty = false;
+  fa_status st = key_weights_sizes(B, Hq, Hkv, Nq, Nk, d, scale, &empty);
+  if (st != FA_OK || empty) return st;
+  const KeyWPlan pl = key_weights_plan(B, Hq, Hkv, Nq, Nk);
+  if (!k || !weights_out || !workspace || (Nq > 0 && (!q || !lse))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned4(lse) || !aligned4(lengths) || !aligned4(weights) ||
+      !aligned4(weights_out))
+    return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.part_bytes)
+    return FA_ERR_INVALID_ARG;
+  const size_t wbytes = (size_t)B * Hkv * Nk * 4;
+  const Range ins[5] = {span(q, (size_t)B * Hq * Nq * d * 2), span(k, (size_t)B * Hkv * Nk * d * 2),
+                        span(lse, (size_t)B * Hq * Nq * 4), span(lengths, lengths ? (size_t)B * 4 : 0),
+                        span(weights, weights && weights != weights_out ? wbytes : 0)};
+  const Range outs[2] = {span(weights_out, wbytes), span(workspace, pl.part_bytes)};
+  if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  st = current_device(&di);
+  if (st != FA_OK) return st;
+  CUtensorMap tq{}, tk{};
+  if (!make_map(&tk, k, (uint64_t)B * Hkv * Nk, d, 128)) return FA_ERR_CUDA;
+  if (Nq > 0 && !make_map(&tq, q, (uint64_t)B * Hq * Nq, d, 128)) return FA_ERR_CUDA;
+  fa::KeyWParams p{};
+  p.lse = lse;
+  p.lengths = lengths;
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.part = pl.n_run > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Nq = Nq;
+  p.Ncap = Nk;
+  p.key_tiles = pl.key_tiles;
+  p.q_tiles = pl.q_tiles;
+  p.n_run = pl.n_run;
+  p.steps_per_run = pl.steps_per_run;
+  p.causal = causal != 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
+  p.err = di->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (d) {
+    case 64: return launch_key_weights<64>(tq, tk, p, s);
+    case 128: return launch_key_weights<128>(tq, tk, p, s);
+    default: return launch_key_weights<256>(tq, tk, p, s);
+  }
+}
+
+fa_status fa_cache_evict(const void* k, const void* v, const float* weights, const int* lengths, void* k_out,
+                         void* v_out, float* weights_out, int* index, int* lengths_out, int B, int Hkv, int Nk,
+                         int out_cap, int budget, int recent, int d, void* stream) {
+  if (B < 0 || Hkv <= 0 || Nk < 0 || d <= 0 || budget < 1 || recent < 0 || recent > budget || out_cap < budget)
+    return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (B == 0) return FA_OK;
+  if ((long long)B * Hkv > 65535 || (long long)B * Hkv * Nk > kIndexLimit ||
+      (long long)B * Hkv * out_cap > kIndexLimit)
+    return FA_ERR_UNSUPPORTED;
+  if (!k_out || !v_out || !weights_out || !index || !lengths_out || (Nk > 0 && (!k || !v || !weights)))
+    return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {k, v, (const void*)k_out, (const void*)v_out})
+    if (!aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)weights, (const void*)lengths, (const void*)weights_out, (const void*)index,
+                          (const void*)lengths_out})
+    if (!aligned4(ptr)) return FA_ERR_INVALID_ARG;
+  const size_t rows = (size_t)B * Hkv * Nk, orows = (size_t)B * Hkv * out_cap;
+  const Range ins[4] = {span(k, rows * d * 2), span(v, rows * d * 2), span(weights, rows * 4),
+                        span(lengths, lengths ? (size_t)B * 4 : 0)};
+  const Range outs[5] = {span(k_out, orows * d * 2), span(v_out, orows * d * 2), span(weights_out, orows * 4),
+                         span(index, orows * 4), span(lengths_out, (size_t)B * 4)};
+  if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  const fa_status st = current_device(&di);
+  if (st != FA_OK) return st;
+  fa::EvictParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.weights = weights;
+  p.lengths = lengths;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.weights_out = weights_out;
+  p.index = index;
+  p.lengths_out = lengths_out;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Ncap = Nk;
+  p.out_cap = out_cap;
+  p.budget = budget;
+  p.recent = recent;
+  p.err = di->err;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned units = (unsigned)(B * Hkv);
+  fa::fa_evict_select_kernel<<<units, fa::kEvictThreads, 0, s>>>(p);
+  if (launched() != FA_OK) return FA_ERR_CUDA;
+  const dim3 grid((unsigned)((budget + fa::kEvictCopyRows - 1) / fa::kEvictCopyRows), units);
+  switch (d) {
+    case 64: fa::fa_evict_copy_kernel<64><<<grid, 256, 0, s>>>(p); break;
+    case 128: fa::fa_evict_copy_kernel<128><<<grid, 256, 0, s>>>(p); break;
+    default: fa::fa_evict_copy_kernel<256><<<grid, 256, 0, s>>>(p); break;
+  }
+  return launched();
+}
+
+}  // extern "C"

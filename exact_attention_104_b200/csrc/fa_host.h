@@ -92,6 +92,10 @@ inline std::mutex g_dev_mu;
 // error word every kernel of the library records into.
 fa_status current_device(DeviceInfo** out);
 
+// Debug builds: the word of fa_cache.cu's own bulk-copy checks (each
+// translation unit has its g_fa_err), which fa_device_status reads too.
+cudaError_t cache_check_word(int** out);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Range {

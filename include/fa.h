@@ -224,6 +224,83 @@ fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, const void*
                         int d, int causal, float scale, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving from key/value caches with room to grow.
+ *
+ * The four calls below share these rules.  A cache is [B, Hkv, Ncap, d] (own
+ * keys of B sequences, Ncap rows of room for each); `lengths` (int32 [B] in
+ * DEVICE memory, or NULL: every sequence fills its cache) says how many rows
+ * of it are keys, 0 <= lengths[b] <= Ncap.  What the cache holds behind them
+ * is never used, whatever it is.  The Nq query rows of a head are the last Nq
+ * positions of the sequence: with L keys in all, row i sits at position
+ * L - Nq + i and with `causal` != 0 sees keys 0 .. L - Nq + i; without, it sees
+ * all L.  A row that sees no key (a sequence shorter than Nq, an empty one)
+ * has O = 0 and LSE = -infinity and gives no key any weight.
+ * lengths is checked on the device: where lengths[b] breaks its rule,
+ * fa_device_status() reports FA_ERR_INVALID_ARG and the outputs of sequence b
+ * are left as they were (those of the others are valid).
+ * Keys, values and queries have to be finite.
+ * bf16 tensors and lse are 16-byte aligned, other fp32 and int32 tensors
+ * 4-byte; `workspace` (device, 256-byte aligned, of at least the size that the
+ * call's *_workspace_bytes function gives; 0 for invalid sizes) is scratch
+ * that is in use until the call's kernels have finished, its contents on entry
+ * do not matter.  Results do not depend on timing: the same inputs give the
+ * same bits.  Other errors as for fa_fwd; B == 0 is a no-op, and Nq == 0 leaves
+ * weights_out equal to weights and writes nothing else.
+ *
+ * Decoding for a batch that shares a prefix: sequence b is the Np keys of the
+ * prefix (k_prefix, v_prefix: bf16 [Hkv, Np, d], one copy for the batch)
+ * followed by its own lengths[b] keys out of k, v [B, Hkv, Ncap, d], so
+ * L = Np + lengths[b].  The prefix is read once for all sequences' rows rather
+ * than once for each.  Np == 0 (k_prefix, v_prefix may be NULL) is decoding
+ * over ragged caches; Ncap == 0 (k, v may be NULL) decoding over the prefix
+ * alone.  q, o bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] (natural log);
+ * Nq <= 256.  The softmax is put together from the key runs' partial results
+ * as in fa_fwd_decode. */
+size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d);
+fa_status fa_fwd_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                               const void* v, const int* lengths, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                               int Np, int Ncap, int d, int causal, float scale, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Decoding that adds up the attention weight of every key: O and LSE as above
+ * (no prefix, Ncap = Nk), and
+ *   weights_out[b,g,j] = weights[b,g,j] + sum of exp(S_ij - LSE_i)
+ * over the Hq/Hkv query heads of kv head g and their Nq rows i that see key j.
+ * weights, weights_out: fp32 [B, Hkv, Nk]; weights NULL counts from zero, and
+ * weights_out == weights updates in place (any other overlap is refused).
+ * Entries j >= lengths[b] of weights_out are those of weights. */
+size_t fa_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, const int* lengths, const float* weights,
+                                float* weights_out, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same weights from queries whose LSE is known: those of a prompt after
+ * fa_fwd (Nq == Nk == N), or of its last Nq positions.  Any Nq >= 0.  lse fp32 [B, Hq, Nq], natural log, as fa_fwd
+ * writes it for the same q, k, causal and scale.  In a padded batch, query rows
+ * end with the sequence as everywhere here: row i of sequence b is position
+ * lengths[b] - Nq + i, and rows whose position is negative give no weight when
+ * causal (whatever their q and lse hold). */
+size_t fa_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+fa_status fa_key_weights(const void* q, const void* k, const float* lse, const int* lengths, const float* weights,
+                         float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated weight.  Of the n = lengths[b] keys of a sequence and
+ * kv head, count = min(n, budget) stay: where n > budget, the last `recent` and,
+ * of the others, the budget - recent of greatest weight (equal weights: the
+ * lower index first; NaN counts as the least).  They keep their order and are
+ * written to slots 0 .. count - 1 of k_out, v_out (bf16 [B, Hkv, out_cap, d])
+ * and weights_out (fp32 [B, Hkv, out_cap]); index (int32 [B, Hkv, out_cap])
+ * gets the slot each came from and lengths_out (int32 [B]) the count.  Slots
+ * count .. budget - 1 are set to zero (index: -1); slots budget .. out_cap - 1
+ * are left as they were, so a larger out_cap leaves room to decode into.
+ * 1 <= budget <= out_cap, 0 <= recent <= budget.  No output may overlap an
+ * input. */
+fa_status fa_cache_evict(const void* k, const void* v, const float* weights, const int* lengths, void* k_out,
+                         void* v_out, float* weights_out, int* index, int* lengths_out, int B, int Hkv, int Nk,
+                         int out_cap, int budget, int recent, int d, void* stream);
+
 /* Size in bytes of the fixed device scratch array used by fa_bwd_noalloc. */
 #define FA_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 
