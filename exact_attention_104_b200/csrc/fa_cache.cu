@@ -213,46 +213,57 @@ fa_status key_weights_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float
   }
   if (B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
   if (Nq > 0 && (long long)B * Hq > kIndexLimit / Nq) return FA_ERR_UNSUPPORTED;
-  if ((long long)B * Hkv > 65535 || (long long)B * Hkv * pad128(Nk) > kIndexLimit) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > 65535 || (long long)B * Hkv * (Nk + 255LL) > kIndexLimit) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
-// Steps (head, 128 query rows) of a key tile are cut into runs of at least 8
-// where the key tiles alone give fewer than about two CTAs an SM.
+// Pure functions of the sizes, so that the workspace sizes need no device.
+constexpr int kKeyWCtas = 148;
 struct KeyWPlan {
-  int key_tiles, q_tiles, n_run, steps_per_run;
-  size_t part_bytes;
+  bool resident;
+  int keys, units, row_tiles;  // keys of a unit
+  size_t part_bytes, range_bytes;
+  size_t total() const { return part_bytes + range_bytes; }
 };
-KeyWPlan key_weights_plan(int B, int Hq, int Hkv, int Nq, int Nk) {
+template <class Res, class Str>
+KeyWPlan key_weights_plan_of(int B, int Hq, int Hkv, int Nq, int Nk) {
   KeyWPlan pl;
-  pl.key_tiles = (Nk + 127) / 128;
-  pl.q_tiles = (Nq + 127) / 128;
-  const long long steps = std::max<long long>(1, (long long)(Hq / Hkv) * pl.q_tiles);
-  const long long units = (long long)B * Hkv * pl.key_tiles;
-  const long long want = std::max<long long>(1, (2 * 148 + units - 1) / units);
-  const long long spr = std::max<long long>(std::min<long long>(8, steps), (steps + want - 1) / want);
-  pl.steps_per_run = (int)std::min<long long>(spr, 1LL << 30);
-  pl.n_run = (int)((steps + pl.steps_per_run - 1) / pl.steps_per_run);
-  pl.part_bytes = pl.n_run > 1 ? round256((size_t)pl.n_run * B * Hkv * pl.key_tiles * 128 * 4) : 0;
+  pl.row_tiles = (int)(((long long)(Hq / Hkv) * Nq + Res::BN - 1) / Res::BN);
+  pl.resident = pl.row_tiles <= Res::NRES;
+  pl.keys = pl.resident ? Res::KEYS : Str::KEYS;
+  pl.units = (Nk + pl.keys - 1) / pl.keys;
+  const size_t units = (size_t)B * Hkv * pl.units;
+  pl.part_bytes = round256((units + kKeyWCtas) * Res::NWG * pl.keys * 4);
+  pl.range_bytes = round256(units * sizeof(int2));
   return pl;
 }
+KeyWPlan key_weights_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  switch (d) {
+    case 64: return key_weights_plan_of<fa::KeyWCfg<64, true>, fa::KeyWCfg<64, false>>(B, Hq, Hkv, Nq, Nk);
+    case 128: return key_weights_plan_of<fa::KeyWCfg<128, true>, fa::KeyWCfg<128, false>>(B, Hq, Hkv, Nq, Nk);
+    default: return key_weights_plan_of<fa::KeyWCfg<256, true>, fa::KeyWCfg<256, false>>(B, Hq, Hkv, Nq, Nk);
+  }
+}
 
-template <int D>
-fa_status launch_key_weights(const CUtensorMap& tq, const CUtensorMap& tk, const fa::KeyWParams& p, cudaStream_t s) {
-  using C = fa::KeyWCfg<D>;
-  auto kern = fa::fa_key_weights_kernel<D>;
+template <int D, bool RESIDENT>
+fa_status launch_key_weights(const void* q, const void* k, const fa::KeyWParams& p, cudaStream_t s) {
+  using C = fa::KeyWCfg<D, RESIDENT>;
+  CUtensorMap tq{}, tk{};
+  if (!make_map(&tk, k, (uint64_t)p.B * p.Hkv * p.Ncap, D, 128)) return FA_ERR_CUDA;
+  if (p.Nq > 0 && !make_map(&tq, q, (uint64_t)p.B * p.Hq * p.Nq, D, C::BN)) return FA_ERR_CUDA;
+  auto kern = fa::fa_key_weights_kernel<D, RESIDENT>;
   static std::atomic<unsigned long long> allowed{0};
   const fa_status st = allow_smem(kern, C::SMEM_BYTES, allowed);
   if (st != FA_OK) return st;
-  const long long ctas = (long long)p.B * p.Hkv * p.key_tiles * p.n_run;
-  if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
-  kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, s>>>(tq, tk, p);
+  kern<<<(unsigned)p.n_ctas, C::THREADS, C::SMEM_BYTES, s>>>(tq, tk, p);
   if (launched() != FA_OK) return FA_ERR_CUDA;
-  if (p.n_run > 1) {
-    fa::fa_key_weights_reduce_kernel<<<dim3((unsigned)((p.Ncap + 255) / 256), (unsigned)(p.B * p.Hkv)), 256, 0, s>>>(p);
-    return launched();
-  }
-  return FA_OK;
+  fa::fa_key_weights_reduce_kernel<C>
+      <<<dim3((unsigned)((p.Ncap + 255) / 256), (unsigned)(p.B * p.Hkv)), 256, 0, s>>>(p);
+  return launched();
+}
+template <int D>
+fa_status launch_key_weights(const void* q, const void* k, const fa::KeyWParams& p, bool resident, cudaStream_t s) {
+  return resident ? launch_key_weights<D, true>(q, k, p, s) : launch_key_weights<D, false>(q, k, p, s);
 }
 
 }  // namespace
@@ -298,7 +309,7 @@ fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, con
 size_t fa_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   bool empty = false;
   if (key_weights_sizes(B, Hq, Hkv, Nq, Nk, d, 1.f, &empty) != FA_OK) return 0;
-  return empty ? 256 : std::max<size_t>(256, key_weights_plan(B, Hq, Hkv, Nq, Nk).part_bytes);
+  return empty ? 256 : key_weights_plan(B, Hq, Hkv, Nq, Nk, d).total();
 }
 
 fa_status fa_key_weights(const void* q, const void* k, const float* lse, const int* lengths, const float* weights,
@@ -307,50 +318,47 @@ fa_status fa_key_weights(const void* q, const void* k, const float* lse, const i
   bool empty = false;
   fa_status st = key_weights_sizes(B, Hq, Hkv, Nq, Nk, d, scale, &empty);
   if (st != FA_OK || empty) return st;
-  const KeyWPlan pl = key_weights_plan(B, Hq, Hkv, Nq, Nk);
+  const KeyWPlan pl = key_weights_plan(B, Hq, Hkv, Nq, Nk, d);
   if (!k || !weights_out || !workspace || (Nq > 0 && (!q || !lse))) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned4(lse) || !aligned4(lengths) || !aligned4(weights) ||
       !aligned4(weights_out))
     return FA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.part_bytes)
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.total())
     return FA_ERR_INVALID_ARG;
   const size_t wbytes = (size_t)B * Hkv * Nk * 4;
   const Range ins[5] = {span(q, (size_t)B * Hq * Nq * d * 2), span(k, (size_t)B * Hkv * Nk * d * 2),
                         span(lse, (size_t)B * Hq * Nq * 4), span(lengths, lengths ? (size_t)B * 4 : 0),
                         span(weights, weights && weights != weights_out ? wbytes : 0)};
-  const Range outs[2] = {span(weights_out, wbytes), span(workspace, pl.part_bytes)};
+  const Range outs[2] = {span(weights_out, wbytes), span(workspace, pl.total())};
   if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   st = current_device(&di);
   if (st != FA_OK) return st;
-  CUtensorMap tq{}, tk{};
-  if (!make_map(&tk, k, (uint64_t)B * Hkv * Nk, d, 128)) return FA_ERR_CUDA;
-  if (Nq > 0 && !make_map(&tq, q, (uint64_t)B * Hq * Nq, d, 128)) return FA_ERR_CUDA;
   fa::KeyWParams p{};
   p.lse = lse;
   p.lengths = lengths;
   p.weights = weights;
   p.weights_out = weights_out;
-  p.part = pl.n_run > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.part = static_cast<float*>(workspace);
+  p.range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + pl.part_bytes);
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.Nq = Nq;
   p.Ncap = Nk;
-  p.key_tiles = pl.key_tiles;
-  p.q_tiles = pl.q_tiles;
-  p.n_run = pl.n_run;
-  p.steps_per_run = pl.steps_per_run;
+  p.units = pl.units;
+  p.row_tiles = pl.row_tiles;
+  p.n_ctas = kKeyWCtas;
   p.causal = causal != 0;
   p.scale_log2 = scale * fa::kLog2e;
   p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
   p.err = di->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (d) {
-    case 64: return launch_key_weights<64>(tq, tk, p, s);
-    case 128: return launch_key_weights<128>(tq, tk, p, s);
-    default: return launch_key_weights<256>(tq, tk, p, s);
+    case 64: return launch_key_weights<64>(q, k, p, pl.resident, s);
+    case 128: return launch_key_weights<128>(q, k, p, pl.resident, s);
+    default: return launch_key_weights<256>(q, k, p, pl.resident, s);
   }
 }
 

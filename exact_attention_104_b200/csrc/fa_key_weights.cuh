@@ -6,50 +6,98 @@
 // Sᵀ = K Qᵀ is computed with the keys as rows, so that a thread of the
 // reading warpgroups owns one key: the sum over query rows runs over the
 // columns of its TMEM lane, in a register, with no exchange between threads.
-// One exponential and half a packed multiply-add and addition per (row, key)
-// pair bound the kernel, not the product (d multiply-adds a pair on the tensor
-// cores).
+// One exponential per (row, key) pair bounds the kernel, not the product (d
+// multiply-adds a pair on the tensor cores): the special-function unit gives
+// 16 a clock and SM, so kKeyWPoly of 8 pairs of exponentials are taken by a
+// polynomial on the FMA pipe instead.
 //
-// One CTA per (128 keys of a sequence's kv head, run of (head, 128 query rows)
-// steps):
-//   warp 0        TMA: the K tile once, then the Q tiles through a ring
-//   warp 1        Sᵀ = K Q_tᵀ into one of four TMEM buffers; TMEM owner
-//   warp 2        −LSE·log2 e of the step's rows into shared memory (−inf for
+// The work is a list of steps, of one row tile (BN query rows) against one
+// unit of keys each, in order of (sequence, kv head, unit of keys, row tile).
+// Every CTA takes an equal run of that list and keeps its TMEM, its rings and
+// its pipeline over the whole run.  The sums of a unit that several CTAs share
+// lie in slot (CTA + unit): along the list each step changes one of the two by
+// one at least, so no two pairs share a slot.  fa_key_weights_reduce_kernel
+// adds the slots of a unit in a fixed order.
+//
+//   resident   all rows of a kv head's group fit NRES row tiles: they stay in
+//              shared memory while the keys stream past, 128 to a unit
+//   streaming  256 keys stay, the rows stream past; each row tile is used for
+//              two products, which halves the traffic from L2
+// With the causal mask a streaming unit that starts at the first query's
+// position or behind it takes, of each head, the rows from the first that sees
+// the unit.
+//
+//   warp 0        TMA: K tiles and Q tiles through two rings
+//   warp 1        Sᵀ = K Qᵀ into one of NBUF TMEM buffers; TMEM owner
+//   warps 2, 3    −LSE·log2 e of the step's rows into shared memory (−inf for
 //                 rows past Nq and rows that see no key at all: weight 0)
-//   warps 4-11    two warpgroups, alternate steps; thread = key
-// Where the steps of a key tile are cut into several runs, each CTA writes its
-// sum and fa_key_weights_reduce_kernel adds them in a fixed order.
+//   warps 4-15    three warpgroups, a 128-key part of a step each in turn;
+//                 thread = key
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
-template <int D>
+constexpr int kKeyWPoly = 2;
+
+// 2^x of two numbers on the FMA and integer pipes.  As exp2_poly, with a
+// quintic (relative error 1.7e-7 in fp32, constant term pinned to 1, c1..c5
+// fitted to 2^f on [−1/2, 1/2] by iteratively reweighted least squares on the
+// relative error).  Clamped at −127: the result there is exactly 0, the
+// product of an exponent field of 0 and a mantissa of 0.  x must be below 128.
+__device__ __forceinline__ uint64_t exp2_poly5(uint64_t x) {
+  float a, b;
+  f2_split(x, a, b);
+  x = f2_make(fmaxf(a, -127.f), fmaxf(b, -127.f));
+  const uint64_t magic = f2_make(12582912.f, 12582912.f), neg_magic = f2_make(-12582912.f, -12582912.f);
+  const uint64_t r = f2_add(x, magic);
+  const uint64_t f = f2_fma(f2_add(r, neg_magic), f2_make(-1.f, -1.f), x);
+  uint64_t p = f2_fma(f2_make(0.001326472731307149f, 0.001326472731307149f), f,
+                      f2_make(0.009671512991189957f, 0.009671512991189957f));
+  p = f2_fma(p, f, f2_make(0.05550733581185341f, 0.05550733581185341f));
+  p = f2_fma(p, f, f2_make(0.24022242426872253f, 0.24022242426872253f));
+  p = f2_fma(p, f, f2_make(0.6931470036506653f, 0.6931470036506653f));
+  p = f2_fma(p, f, f2_make(1.f, 1.f));
+  float r0, r1, p0, p1;
+  f2_split(r, r0, r1);
+  f2_split(p, p0, p1);
+  return f2_make(__int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23)),
+                 __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23)));
+}
+
+template <int D, bool RESIDENT>
 struct KeyWCfg {
-  static constexpr int THREADS = 384;
-  static constexpr int BM = 128;  // keys (MMA M)
-  static constexpr int BN = 128;  // query rows of a step (MMA N)
-  static constexpr int PANEL = 128 * 128;
-  static constexpr int TILE = BM * D * 2;
-  static constexpr int NST = D == 64 ? 6 : (D == 128 ? 4 : 2);
-  static constexpr int NBUF = 4;  // TMEM buffers of Sᵀ, and of the rows' −LSE
+  static constexpr int THREADS = 512;
+  static constexpr int NWG = 3;                     // reading warpgroups
+  static constexpr int BN = D == 256 ? 64 : 128;    // query rows of a step (MMA N)
+  static constexpr int KU = RESIDENT ? 1 : 2;       // 128-key tiles of a unit
+  static constexpr int KEYS = 128 * KU;
+  static constexpr int R = KEYS / BN;               // row tiles in a unit's length
+  static constexpr int KPANEL = 128 * 128, QPANEL = BN * 128;  // 64 columns (bytes)
+  static constexpr int KTILE = 128 * D * 2, QTILE = BN * D * 2;
+  static constexpr int NRES = D == 64 ? 4 : 2;      // row tiles that fit beside the K ring
+  static constexpr int NK = RESIDENT ? (D == 64 ? 8 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : 2);
+  static constexpr int NQ = RESIDENT ? NRES : (D == 64 ? 8 : (D == 128 ? 4 : 2));
+  static constexpr int NBUF = 512 / BN;             // TMEM buffers of Sᵀ
+  static constexpr int NL = 4;                      // buffers of the rows' −LSE
   static constexpr int K_OFF = 0;
-  static constexpr int Q_OFF = TILE;
-  static constexpr int LSE_OFF = Q_OFF + NST * TILE;
-  static constexpr int SUM_OFF = LSE_OFF + NBUF * BN * 4;
-  static constexpr int BAR_OFF = SUM_OFF + BM * 4;
+  static constexpr int Q_OFF = NK * KTILE;
+  static constexpr int LSE_OFF = Q_OFF + NQ * QTILE;
+  static constexpr int BAR_OFF = LSE_OFF + NL * BN * 4;
   static constexpr int B_KFULL = 0;
-  static constexpr int B_QFULL = 1;
-  static constexpr int B_QEMPTY = B_QFULL + NST;
-  static constexpr int B_SFULL = B_QEMPTY + NST;
+  static constexpr int B_KEMPTY = B_KFULL + NK;
+  static constexpr int B_QFULL = B_KEMPTY + NK;
+  static constexpr int B_QEMPTY = B_QFULL + NQ;
+  static constexpr int B_SFULL = B_QEMPTY + NQ;
   static constexpr int B_SEMPTY = B_SFULL + NBUF;
   static constexpr int B_LFULL = B_SEMPTY + NBUF;
-  static constexpr int B_DRAIN = B_LFULL + NBUF;
+  static constexpr int B_LEMPTY = B_LFULL + NL;
+  static constexpr int B_DRAIN = B_LEMPTY + NL;
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;
   static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
-  static constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN, false, false);
+  static constexpr uint32_t IDESC = idesc_bf16_f32(128, BN, false, false);
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
@@ -58,9 +106,12 @@ struct KeyWParams {
   const int* lengths;    // [B], or null
   const float* weights;  // [B, Hkv, Ncap], or null
   float* weights_out;
-  float* part;           // [n_run][B·Hkv][key_tiles·128], or null with one run
+  float* part;           // [n_ctas + B·Hkv·units][NWG][KEYS] sums
+  int2* range;           // [B·Hkv·units] first and last CTA of the unit
   int B, Hq, Hkv, G, Nq, Ncap;
-  int key_tiles, q_tiles, n_run, steps_per_run;
+  int units;             // units of keys of a full cache
+  int row_tiles;         // of all rows of a group: ceil(G·Nq / BN)
+  int n_ctas;
   int causal;
   float scale_log2;
   long long wait_cap;
@@ -72,46 +123,138 @@ __device__ __forceinline__ int keyw_len(const KeyWParams& p, int b) {
   return (n < 0 || n > p.Ncap) ? -1 : n;
 }
 
-// First 128-row query tile that sees any key of tile j0 .. j0+127, and the
-// number of steps (head, query tile) of that key tile.
-__device__ __forceinline__ void keyw_steps(const KeyWParams& p, int len, int j0, int& qt0, int& n) {
-  qt0 = 0;
-  if (p.causal) {
-    const int i0 = j0 - (len - p.Nq);  // row i sees key j0 when i >= i0
-    qt0 = i0 > 0 ? i0 / 128 : 0;
+// The steps of one sequence's kv head.  Units 0 .. whole−1 take all rows of
+// the group, packed (row r = h·Nq + i); a later unit u takes per head the rows
+// from i0 = u·KEYS − (len − Nq) on, which are len − u·KEYS.
+template <class C>
+struct KeyWSeq {
+  int len, units, whole, kb;  // kb: row tiles in len keys
+  __device__ __forceinline__ void set(const KeyWParams& p, int b) {
+    len = b < p.B ? keyw_len(p, b) : 0;
+    units = len > 0 && p.row_tiles > 0 ? (len + C::KEYS - 1) / C::KEYS : 0;
+    kb = (len + C::BN - 1) / C::BN;
+    whole = units;
+    if (p.causal && C::KU == 2) whole = len > p.Nq ? min(units, (len - p.Nq + C::KEYS - 1) / C::KEYS) : 0;
   }
-  n = j0 < len && qt0 < p.q_tiles ? p.G * (p.q_tiles - qt0) : 0;
-}
+  __device__ __forceinline__ int head_tiles(int u) const { return kb - C::R * u; }
+  __device__ __forceinline__ int steps(const KeyWParams& p, int u) const {
+    return u < whole ? p.row_tiles : p.G * head_tiles(u);
+  }
+  // steps of units 0 .. units−1
+  __device__ __forceinline__ long long total(const KeyWParams& p) const {
+    const long long m = units - whole;
+    return (long long)whole * p.row_tiles + p.G * (m * kb - C::R * (m * (whole + units - 1) / 2));
+  }
+};
 
-template <int D>
-__global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
+// Position in the list of steps; every role of a CTA walks the same run.
+template <class C>
+struct KeyWIter {
+  KeyWSeq<C> seq;
+  int b, hkv, u, s, n;  // step s of the n of unit u
+  int h, t, tiles;      // per-head units: head, row tile of the head and their number
+  int left;             // steps of this CTA, this one included
+
+  __device__ __forceinline__ void unit() {
+    if (u < seq.whole) return;
+    tiles = seq.head_tiles(u);
+    h = s / tiles;
+    t = s - h * tiles;
+  }
+  // This CTA's run; false if it is empty.  The whole warp calls it.
+  __device__ __forceinline__ bool start(const KeyWParams& p, int cta) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      seq.set(p, b0 + lane);
+      if (seq.len < 0 && cta == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
+      all += seq.total(p);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    all *= p.Hkv;
+    const long long per = (all + p.n_ctas - 1) / p.n_ctas;
+    long long x = per * cta;
+    if (x >= all) return false;
+    left = (int)(min(all, x + per) - x);
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      seq.set(p, b0 + lane);
+      const long long mine = seq.total(p) * p.Hkv;
+      long long sum = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, sum > x);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        x -= __shfl_sync(0xffffffffu, sum - mine, l);
+        break;
+      }
+      x -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    seq.set(p, b);
+    const long long one = seq.total(p);
+    hkv = (int)(x / one);
+    x -= hkv * one;
+    u = 0;
+    if (x < (long long)seq.whole * p.row_tiles) {
+      u = (int)(x / p.row_tiles);
+      x -= (long long)u * p.row_tiles;
+    } else {
+      x -= (long long)seq.whole * p.row_tiles;
+      for (u = seq.whole; x >= seq.steps(p, u); ++u) x -= seq.steps(p, u);
+    }
+    s = (int)x;
+    n = seq.steps(p, u);
+    unit();
+    return true;
+  }
+  // To the next step (call only while left > 1).
+  __device__ __forceinline__ void next(const KeyWParams& p) {
+    --left;
+    if (++s < n) {
+      if (++t == tiles) {
+        t = 0;
+        ++h;
+      }
+      return;
+    }
+    s = 0;
+    if (++u == seq.units) {
+      u = 0;
+      if (++hkv == p.Hkv) {
+        hkv = 0;
+        do seq.set(p, ++b);
+        while (seq.units == 0 && b < p.B);
+      }
+    }
+    n = seq.steps(p, u);
+    unit();
+  }
+  __device__ __forceinline__ bool packed() const { return u < seq.whole; }
+  // First row of the step within the group's G·Nq rows, and how many of the
+  // tile's rows count.
+  __device__ __forceinline__ int row0(const KeyWParams& p) const {
+    return packed() ? s * C::BN : h * p.Nq + u * C::KEYS - (seq.len - p.Nq) + t * C::BN;
+  }
+  __device__ __forceinline__ int rows(const KeyWParams& p) const {
+    return packed() ? min(C::BN, p.G * p.Nq - s * C::BN) : min(C::BN, seq.len - u * C::KEYS - t * C::BN);
+  }
+  __device__ __forceinline__ bool unit_ends() const { return left == 1 || s == n - 1; }
+  __device__ __forceinline__ bool head_ends() const { return left == 1 || (s == n - 1 && u == seq.units - 1); }
+};
+
+template <int D, bool RESIDENT>
+__global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
     fa_key_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const KeyWParams p) {
-  using C = KeyWCfg<D>;
-  const int run = blockIdx.x % p.n_run;
-  const int jt = blockIdx.x / p.n_run % p.key_tiles;
-  const int unit = blockIdx.x / p.n_run / p.key_tiles;
-  const int b = unit / p.Hkv, hkv = unit % p.Hkv;
-  const int j0 = jt * 128;
-  const int len = keyw_len(p, b);
-  if (len < 0) {  // a length out of range: this sequence's weights are not written
-    if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
-    return;
-  }
-  int qt0, n_all;
-  keyw_steps(p, len, j0, qt0, n_all);
-  const int s0 = run * p.steps_per_run;
-  const int n = min(n_all - s0, p.steps_per_run);
-  const int nq = p.q_tiles - qt0;  // query tiles of a head (positive where n > 0)
-  if (n <= 0) {
-    // nothing visible: the weights stay as they were (one run: written here)
-    const int j = j0 + threadIdx.x;
-    if (p.n_run == 1 && threadIdx.x < 128 && j < p.Ncap) {
-      const size_t at = (size_t)unit * p.Ncap + j;
-      p.weights_out[at] = p.weights ? p.weights[at] : 0.f;
-    }
-    return;
-  }
+  using C = KeyWCfg<D, RESIDENT>;
+  KeyWIter<C> it;
+  const int cta = blockIdx.x;
+  if (!it.start(p, cta)) return;  // the same for every warp
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -120,19 +263,24 @@ __global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   float* lse_s = reinterpret_cast<float*>(smem + C::LSE_OFF);
-  float* sum_s = reinterpret_cast<float*>(smem + C::SUM_OFF);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(BAR(C::B_KFULL), 1);
-    for (int i = 0; i < C::NST; ++i) {
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(BAR(C::B_KFULL + i), 1);
+      mbar_init(BAR(C::B_KEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::NQ; ++i) {
       mbar_init(BAR(C::B_QFULL + i), 1);
       mbar_init(BAR(C::B_QEMPTY + i), 1);
     }
     for (int i = 0; i < C::NBUF; ++i) {
       mbar_init(BAR(C::B_SFULL + i), 1);
       mbar_init(BAR(C::B_SEMPTY + i), 4);
+    }
+    for (int i = 0; i < C::NL; ++i) {
       mbar_init(BAR(C::B_LFULL + i), 1);
+      mbar_init(BAR(C::B_LEMPTY + i), 4 * C::KU);
     }
     mbar_init(BAR(C::B_DRAIN), 1);
     *abort_flag = 0;
@@ -147,123 +295,241 @@ __global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_holder;
   const WaitCtx wc{abort_flag, p.err, p.wait_cap};
-  // step t of this CTA -> first row of its Q tile within the head, and the head
-  auto step_head = [&](int t) { return hkv * p.G + (s0 + t) / nq; };
-  auto step_row = [&](int t) { return (qt0 + (s0 + t) % nq) * 128; };
 
-  float sum = 0.f;
   if (warp == 0) {
     if (lane == 0) {
-      mbar_expect_tx(BAR(C::B_KFULL), C::TILE);
-#pragma unroll
-      for (int pn = 0; pn < D / 64; ++pn)
-        tma_load_2d(sbase + C::K_OFF + pn * C::PANEL, &tmK, BAR(C::B_KFULL), pn * 64, unit * p.Ncap + j0);
-      int issued = 0;
-      for (int t = 0; t < n; ++t) {
-        const int st = t % C::NST;
-        if (!mbar_wait(BAR(C::B_QEMPTY + st), ((t / C::NST) & 1) ^ 1, wc, 31)) break;
-        mbar_expect_tx(BAR(C::B_QFULL + st), C::TILE);
-        const int y = (b * p.Hq + step_head(t)) * p.Nq + step_row(t);
+      int kseq = 0, qseq = 0;  // tiles issued
+      bool ok = true;
+      auto load_q = [&](int row) -> bool {
+        const int sl = qseq % C::NQ;
+        if (!mbar_wait(BAR(C::B_QEMPTY + sl), ((qseq / C::NQ) & 1) ^ 1, wc, 31)) return false;
+        mbar_expect_tx(BAR(C::B_QFULL + sl), C::QTILE);
+        const int y = (it.b * p.Hq + it.hkv * p.G) * p.Nq + row;
 #pragma unroll
         for (int pn = 0; pn < D / 64; ++pn)
-          tma_load_2d(sbase + C::Q_OFF + st * C::TILE + pn * C::PANEL, &tmQ, BAR(C::B_QFULL + st), pn * 64, y);
-        issued = t + 1;
+          tma_load_2d(sbase + C::Q_OFF + sl * C::QTILE + pn * C::QPANEL, &tmQ, BAR(C::B_QFULL + sl), pn * 64, y);
+        ++qseq;
+        return true;
+      };
+      bool new_unit = true, new_head = true;
+      while (true) {
+        if (RESIDENT && new_head)
+          for (int s = 0; s < p.row_tiles && ok; ++s) ok = load_q(s * C::BN);
+        if (new_unit)
+          for (int k = 0; k < C::KU && ok; ++k) {
+            const int sl = kseq % C::NK;
+            ok = mbar_wait(BAR(C::B_KEMPTY + sl), ((kseq / C::NK) & 1) ^ 1, wc, 32);
+            if (!ok) break;
+            mbar_expect_tx(BAR(C::B_KFULL + sl), C::KTILE);
+            const int y = (it.b * p.Hkv + it.hkv) * p.Ncap + it.u * C::KEYS + k * 128;
+#pragma unroll
+            for (int pn = 0; pn < D / 64; ++pn)
+              tma_load_2d(sbase + C::K_OFF + sl * C::KTILE + pn * C::KPANEL, &tmK, BAR(C::B_KFULL + sl), pn * 64, y);
+            ++kseq;
+          }
+        if (!RESIDENT && ok) ok = load_q(it.row0(p));
+        if (!ok || it.left == 1) break;
+        new_unit = it.unit_ends();
+        new_head = it.head_ends();
+        it.next(p);
       }
       // every load issued has landed before the CTA may exit
-      mbar_wait_inflight(BAR(C::B_KFULL), 0, wc, 32);
-      for (int st = 0; st < C::NST && st < issued; ++st) {
-        const int last = issued - 1 - (issued - 1 - st) % C::NST;
-        mbar_wait_inflight(BAR(C::B_QFULL + st), (last / C::NST) & 1, wc, 33);
-      }
+      for (int i = max(0, kseq - C::NK); i < kseq; ++i)
+        mbar_wait_inflight(BAR(C::B_KFULL + i % C::NK), (i / C::NK) & 1, wc, 33);
+      for (int i = max(0, qseq - C::NQ); i < qseq; ++i)
+        mbar_wait_inflight(BAR(C::B_QFULL + i % C::NQ), (i / C::NQ) & 1, wc, 34);
     }
   } else if (warp == 1) {
-    bool ok = mbar_wait_warp(BAR(C::B_KFULL), 0, wc, 34);
     const uint64_t dk = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
     const uint64_t dq = sdesc_sw128(sbase + C::Q_OFF, 16, 1024);
-    for (int t = 0; t < n && ok; ++t) {
-      const int st = t % C::NST, x = t % C::NBUF;
-      if (!mbar_wait_warp(BAR(C::B_QFULL + st), (t / C::NST) & 1, wc, 35)) break;
-      if (!mbar_wait_warp(BAR(C::B_SEMPTY + x), ((t / C::NBUF) & 1) ^ 1, wc, 36)) break;
-      tc_fence_after();
+    int kseq = 0, qseq = 0, sub = 0;  // first K tile of the unit, Q tile (resident: the group's first), product
+    bool new_unit = true, new_head = true, ok = true;
+    while (true) {
+      if (RESIDENT && new_head)
+        for (int s = 0; s < p.row_tiles && ok; ++s)
+          ok = mbar_wait_warp(BAR(C::B_QFULL + (qseq + s) % C::NQ), ((qseq + s) / C::NQ) & 1, wc, 35);
+      if (new_unit)
+        for (int k = 0; k < C::KU && ok; ++k)
+          ok = mbar_wait_warp(BAR(C::B_KFULL + (kseq + k) % C::NK), ((kseq + k) / C::NK) & 1, wc, 36);
+      if (!RESIDENT && ok) ok = mbar_wait_warp(BAR(C::B_QFULL + qseq % C::NQ), (qseq / C::NQ) & 1, wc, 35);
+      if (!ok) break;
+      const uint32_t qoff = (RESIDENT ? (qseq + it.s) % C::NQ : qseq % C::NQ) * C::QTILE;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * C::PANEL + (kk & 3) * 32;
-        mma_ss_w(tbase + x * 128, sdesc_add(dk, off), sdesc_add(dq, st * C::TILE + off), C::IDESC, kk > 0 ? 1u : 0u);
+      for (int k = 0; k < C::KU; ++k) {
+        const int x = sub % C::NBUF;
+        if (!mbar_wait_warp(BAR(C::B_SEMPTY + x), ((sub / C::NBUF) & 1) ^ 1, wc, 37)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t koff = (kseq + k) % C::NK * C::KTILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_w(tbase + x * C::BN, sdesc_add(dk, koff + (kk >> 2) * C::KPANEL + (kk & 3) * 32),
+                   sdesc_add(dq, qoff + (kk >> 2) * C::QPANEL + (kk & 3) * 32), C::IDESC, kk > 0 ? 1u : 0u);
+        tc_commit_w(BAR(C::B_SFULL + x));
+        ++sub;
       }
-      tc_commit_w(BAR(C::B_SFULL + x));
-      tc_commit_w(BAR(C::B_QEMPTY + st));
+      if (!ok) break;
+      new_unit = it.unit_ends();
+      new_head = it.head_ends();
+      if (!RESIDENT) {
+        tc_commit_w(BAR(C::B_QEMPTY + qseq % C::NQ));
+        ++qseq;
+      } else if (new_head) {
+        for (int s = 0; s < p.row_tiles; ++s) tc_commit_w(BAR(C::B_QEMPTY + (qseq + s) % C::NQ));
+        qseq += p.row_tiles;
+      }
+      if (new_unit) {
+        for (int k = 0; k < C::KU; ++k) tc_commit_w(BAR(C::B_KEMPTY + (kseq + k) % C::NK));
+        kseq += C::KU;
+      }
+      if (it.left == 1) break;
+      it.next(p);
     }
     // no MMA may still be running when TMEM is released
     tc_commit_w(BAR(C::B_DRAIN));
-    mbar_wait_inflight(BAR(C::B_DRAIN), 0, wc, 37);
-  } else if (warp == 2) {
-    for (int t = 0; t < n; ++t) {
-      const int x = t % C::NBUF;
-      if (!mbar_wait_warp(BAR(C::B_SEMPTY + x), ((t / C::NBUF) & 1) ^ 1, wc, 38)) break;
-      const float* src = p.lse + ((size_t)b * p.Hq + step_head(t)) * p.Nq;
-      const int i0 = step_row(t);
+    mbar_wait_inflight(BAR(C::B_DRAIN), 0, wc, 38);
+  } else if (warp < 4) {
+    for (int q = 0;; ++q) {
+      if ((q & 1) == warp - 2) {
+        const float* src = p.lse + ((size_t)it.b * p.Hq + it.hkv * p.G) * p.Nq + it.row0(p);
+        const int rows = it.rows(p);
+        float v[C::BN / 32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int i = i0 + c * 32 + lane;
-        float v = -INFINITY;
-        if (i < p.Nq) {
-          v = -src[i] * kLog2e;
-          if (v == INFINITY) v = -INFINITY;
+        for (int c = 0; c < C::BN / 32; ++c) {
+          v[c] = -INFINITY;
+          if (c * 32 + lane < rows) {
+            v[c] = -src[c * 32 + lane] * kLog2e;
+            if (v[c] == INFINITY) v[c] = -INFINITY;
+          }
         }
-        lse_s[x * 128 + c * 32 + lane] = v;
+        if (!mbar_wait_warp(BAR(C::B_LEMPTY + q % C::NL), ((q / C::NL) & 1) ^ 1, wc, 39)) break;
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) lse_s[q % C::NL * C::BN + c * 32 + lane] = v[c];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::B_LFULL + q % C::NL));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::B_LFULL + x));
+      if (it.left == 1) break;
+      it.next(p);
     }
-  } else if (warp >= 4) {
+  } else {
     const int grp = (warp - 4) >> 2, quarter = warp & 3;
-    const int key = j0 + quarter * 32 + lane;
+    const int mykey = quarter * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint64_t sl2 = f2_make(p.scale_log2, p.scale_log2);
-    uint64_t acc[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-    for (int t = grp; t < n; t += 2) {
-      const int x = t % C::NBUF;
-      const uint32_t par = (t / C::NBUF) & 1;
-      if (!mbar_wait_warp(BAR(C::B_LFULL + x), par, wc, 39)) break;
-      if (!mbar_wait_warp(BAR(C::B_SFULL + x), par, wc, 40)) break;
-      tc_fence_after();
-      // rows of the step before column c0 do not see this thread's key
-      int c0 = 0;
-      if (p.causal) c0 = key - (len - p.Nq) - step_row(t);
-      const bool edge = __any_sync(0xffffffffu, c0 > 0);
+    float sum[C::KU];
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t r[32];
-        tmem_ld32(tl + x * 128 + cc * 32, r);
-        const float4* ng = reinterpret_cast<const float4*>(lse_s + x * 128 + cc * 32);
-        tmem_ld_wait();
-        reg_fence(r);
+    for (int k = 0; k < C::KU; ++k) sum[k] = 0.f;
+    bool ok = true;
+    for (int q = 0; ok; ++q) {
+      const int key0 = it.u * C::KEYS;
+      if (it.s == 0 && warp == 4 && lane == 0)
+        p.range[((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u].x = cta;
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 g = ng[c / 4];
-          float e0, e1, e2, e3;
-          f2_split(f2_fma(f2_make(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2, f2_make(g.x, g.y)), e0, e1);
-          f2_split(f2_fma(f2_make(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2, f2_make(g.z, g.w)), e2,
-                   e3);
-          if (edge) {
-            if (cc * 32 + c < c0) e0 = -INFINITY;
-            if (cc * 32 + c + 1 < c0) e1 = -INFINITY;
-            if (cc * 32 + c + 2 < c0) e2 = -INFINITY;
-            if (cc * 32 + c + 3 < c0) e3 = -INFINITY;
-          }
-          acc[0] = f2_add(acc[0], f2_make(ex2(e0), ex2(e1)));
-          acc[1] = f2_add(acc[1], f2_make(ex2(e2), ex2(e3)));
+      for (int k = 0; k < C::KU; ++k) {
+        const int sub = q * C::KU + k;
+        if (sub % C::NWG != grp) continue;
+        const int x = sub % C::NBUF, y = q % C::NL;
+        if (!mbar_wait_warp(BAR(C::B_LFULL + y), (q / C::NL) & 1, wc, 40) ||
+            !mbar_wait_warp(BAR(C::B_SFULL + x), (sub / C::NBUF) & 1, wc, 41)) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        // Row i of a head sees key j when i >= j − (len − Nq).  i: number of
+        // the tile's first row; a packed tile may go on with row 0 of the next head
+        const int off = it.seq.len - p.Nq;
+        const int last = key0 + k * 128 + 127;
+        int i = 0;
+        bool cut = p.causal && last > off;  // does the mask cut through the tile?
+        bool none = key0 + k * 128 >= it.seq.len;
+        if (cut) {
+          i = it.packed() ? it.s * C::BN % p.Nq : key0 - off + it.t * C::BN;
+          cut = last - off > (it.packed() && i + C::BN > p.Nq ? 0 : i);
+          none |= !it.packed() && last - 127 - off >= i + C::BN;
+        }
+        // columns past the tile's rows are another head's rows, whatever they hold
+        const int rows = none ? 0 : it.rows(p);
+        // this key is seen from row `need` of its head on
+        const int need = cut ? key0 + k * 128 + mykey - off : 0;
+        int c0 = 0;
+        if (cut && !it.packed()) c0 = max(0, need - lane - i) & ~31;  // blocks that no key of the warp is seen from
+        uint64_t acc[2] = {0, 0};
+#pragma unroll 1
+        for (; c0 < rows; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tl + x * C::BN + c0, r);
+          const float4* ng = reinterpret_cast<const float4*>(lse_s + y * C::BN + c0);
+          uint32_t valid = rows - c0 >= 32 ? 0xffffffffu : (1u << (rows - c0)) - 1u;
+          if (cut) {
+            if (it.packed()) {
+              // the rows' numbers within their heads start anew at Nq
+              uint32_t m = 0;
+#pragma unroll 1
+              for (int c = 0; c < 32; ++c) {
+                m |= (i >= need ? 1u : 0u) << c;
+                if (++i == p.Nq) i = 0;
+              }
+              valid &= m;
+            } else {
+              const int first = need - i - c0;
+              if (first > 0) valid &= first < 32 ? 0xffffffffu << first : 0u;
+            }
+          }
+          tmem_ld_wait();
+          reg_fence(r);
+          if (__all_sync(0xffffffffu, valid == 0xffffffffu)) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 g = ng[c / 4];
+              const uint64_t e0 = f2_fma(f2_make(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
+                                         f2_make(g.x, g.y));
+              const uint64_t e1 = f2_fma(f2_make(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2,
+                                         f2_make(g.z, g.w));
+              // of the pairs 0 .. 7 of 16 columns, kKeyWPoly spread evenly
+              auto exp_pair = [&](uint64_t e, int pr) -> uint64_t {
+                if ((pr * kKeyWPoly) % 8 < kKeyWPoly) return exp2_poly5(e);
+                float a, b2;
+                f2_split(e, a, b2);
+                return f2_make(ex2(a), ex2(b2));
+              };
+              acc[0] = f2_add(acc[0], exp_pair(e0, (c / 2) % 8));
+              acc[1] = f2_add(acc[1], exp_pair(e1, (c / 2 + 1) % 8));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const float2 g = reinterpret_cast<const float2*>(ng)[c / 2];
+              const float e0 = fmaf(__uint_as_float(r[c]), p.scale_log2, g.x);
+              const float e1 = fmaf(__uint_as_float(r[c + 1]), p.scale_log2, g.y);
+              acc[0] = f2_add(acc[0], f2_make(ex2(valid >> c & 1 ? e0 : -INFINITY),
+                                              ex2(valid >> (c + 1) & 1 ? e1 : -INFINITY)));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(BAR(C::B_SEMPTY + x));
+          mbar_arrive(BAR(C::B_LEMPTY + y));
+        }
+        float a, b2, c2, d2;
+        f2_split(acc[0], a, b2);
+        f2_split(acc[1], c2, d2);
+        sum[k] += (a + b2) + (c2 + d2);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::B_SEMPTY + x));
+      if (!ok) break;
+      if (it.unit_ends()) {
+        const size_t unit = ((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u;
+        float* dst = p.part + ((unit + cta) * C::NWG + grp) * C::KEYS + mykey;
+#pragma unroll
+        for (int k = 0; k < C::KU; ++k) {
+          dst[k * 128] = sum[k];
+          sum[k] = 0.f;
+        }
+        if (it.s == it.n - 1 && warp == 4 && lane == 0) p.range[unit].y = cta;
+      }
+      if (it.left == 1) break;
+      it.next(p);
     }
-    float a, c2, d2, e2;
-    f2_split(acc[0], a, c2);
-    f2_split(acc[1], d2, e2);
-    sum = (a + c2) + (d2 + e2);
-    if (grp == 1) sum_s[quarter * 32 + lane] = sum;
   }
 
   tc_fence_before();
@@ -272,33 +538,35 @@ __global__ void __launch_bounds__(KeyWCfg<D>::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
-  if (warp >= 4 && warp < 8 && !*abort_flag) {
-    const int r = (warp & 3) * 32 + lane, j = j0 + r;
-    sum += sum_s[r];
-    if (p.n_run > 1) {
-      p.part[((size_t)run * p.B * p.Hkv + unit) * (p.key_tiles * 128) + j] = sum;
-    } else if (j < p.Ncap) {
-      const size_t at = (size_t)unit * p.Ncap + j;
-      const float w = p.weights ? p.weights[at] : 0.f;
-      p.weights_out[at] = j < len ? w + sum : w;
-    }
-  }
 }
 
-// weights_out = weights + the runs' sums, added in order of the runs.
+// weights_out = weights + the sums of the key's unit, added in order of the
+// CTAs and their warpgroups.
+template <class C>
 __global__ void __launch_bounds__(256) fa_key_weights_reduce_kernel(const KeyWParams p) {
-  const int unit = blockIdx.y, b = unit / p.Hkv;
-  const int j = blockIdx.x * 256 + threadIdx.x;
-  const int len = keyw_len(p, b);
-  if (len < 0 || j >= p.Ncap) return;
-  int qt0, n;
-  keyw_steps(p, len, j / 128 * 128, qt0, n);
-  const int runs = (n + p.steps_per_run - 1) / p.steps_per_run;
-  const size_t at = (size_t)unit * p.Ncap + j;
-  float s = 0.f;
-  for (int r = 0; r < runs; ++r) s += p.part[((size_t)r * p.B * p.Hkv + unit) * (p.key_tiles * 128) + j];
-  const float w = p.weights ? p.weights[at] : 0.f;
-  p.weights_out[at] = j < len ? w + s : w;
+  const int bh = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+  if (j >= p.Ncap) return;
+  KeyWSeq<C> seq;
+  seq.set(p, bh / p.Hkv);
+  if (seq.len < 0) {  // this sequence's weights are not written
+    if (j == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
+    return;
+  }
+  const size_t at = (size_t)bh * p.Ncap + j;
+  float w = p.weights ? p.weights[at] : 0.f;
+  const int u = j / C::KEYS;
+  if (j < seq.len && u < seq.units) {
+    const size_t unit = (size_t)bh * p.units + u;
+    const int2 ctas = p.range[unit];
+    // (within bounds also after a call that gave up)
+    const int c0 = max(ctas.x, 0), c1 = min(ctas.y, p.n_ctas - 1);
+    float s = 0.f;
+    for (int c = c0; c <= c1; ++c)
+#pragma unroll
+      for (int g = 0; g < C::NWG; ++g) s += p.part[((unit + c) * C::NWG + g) * C::KEYS + j % C::KEYS];
+    w += s;
+  }
+  p.weights_out[at] = w;
 }
 
 }  // namespace fa
