@@ -222,8 +222,8 @@ constexpr int kKeyWCtas = 148;
 struct KeyWPlan {
   bool resident;
   int keys, units, row_tiles;  // keys of a unit
-  size_t part_bytes, range_bytes;
-  size_t total() const { return part_bytes + range_bytes; }
+  size_t part_bytes, range_bytes, present_bytes;
+  size_t total() const { return part_bytes + range_bytes + present_bytes; }
 };
 template <class Res, class Str>
 KeyWPlan key_weights_plan_of(int B, int Hq, int Hkv, int Nq, int Nk) {
@@ -235,6 +235,7 @@ KeyWPlan key_weights_plan_of(int B, int Hq, int Hkv, int Nq, int Nk) {
   const size_t units = (size_t)B * Hkv * pl.units;
   pl.part_bytes = round256((units + kKeyWCtas) * Res::NWG * pl.keys * 4);
   pl.range_bytes = round256(units * sizeof(int2));
+  pl.present_bytes = round256(units + kKeyWCtas);
   return pl;
 }
 KeyWPlan key_weights_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
@@ -347,6 +348,7 @@ fa_status fa_key_weights(const void* q, const void* k, const float* lse, const i
   p.G = Hq / Hkv;
   p.Nq = Nq;
   p.Ncap = Nk;
+  p.present = static_cast<uint8_t*>(workspace) + pl.part_bytes + pl.range_bytes;
   p.units = pl.units;
   p.row_tiles = pl.row_tiles;
   p.n_ctas = kKeyWCtas;

@@ -30,7 +30,8 @@
 //   warp 0        TMA: K tiles and Q tiles through two rings
 //   warp 1        Sᵀ = K Qᵀ into one of NBUF TMEM buffers; TMEM owner
 //   warps 2, 3    −LSE·log2 e of the step's rows into shared memory (−inf for
-//                 rows past Nq and rows that see no key at all: weight 0)
+//                 rows past Nq and rows that see no key at all: weight 0), and
+//                 what the readers have to know about the step
 //   warps 4-15    three warpgroups, a 128-key part of a step each in turn;
 //                 thread = key
 #pragma once
@@ -80,11 +81,15 @@ struct KeyWCfg {
   static constexpr int NK = RESIDENT ? (D == 64 ? 8 : (D == 128 ? 4 : 2)) : (D == 64 ? 4 : 2);
   static constexpr int NQ = RESIDENT ? NRES : (D == 64 ? 8 : (D == 128 ? 4 : 2));
   static constexpr int NBUF = 512 / BN;             // TMEM buffers of Sᵀ
-  static constexpr int NL = 4;                      // buffers of the rows' −LSE
+  // buffers of the rows' −LSE and of the steps' KeyWStep.  A wait by parity must
+  // not run a phase ahead: with a multiple of 2 and of NWG, a buffer has one
+  // filling warp and the same reading warpgroups every time
+  static constexpr int NL = 6;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = NK * KTILE;
   static constexpr int LSE_OFF = Q_OFF + NQ * QTILE;
-  static constexpr int BAR_OFF = LSE_OFF + NL * BN * 4;
+  static constexpr int STEP_OFF = LSE_OFF + NL * BN * 4;
+  static constexpr int BAR_OFF = STEP_OFF + NL * 32;
   static constexpr int B_KFULL = 0;
   static constexpr int B_KEMPTY = B_KFULL + NK;
   static constexpr int B_QFULL = B_KEMPTY + NK;
@@ -99,6 +104,7 @@ struct KeyWCfg {
   static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
   static constexpr uint32_t IDESC = idesc_bf16_f32(128, BN, false, false);
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(NL % 2 == 0 && NL % NWG == 0, "one filling warp and fixed readers for a buffer");
 };
 
 struct KeyWParams {
@@ -108,6 +114,7 @@ struct KeyWParams {
   float* weights_out;
   float* part;           // [n_ctas + B·Hkv·units][NWG][KEYS] sums
   int2* range;           // [B·Hkv·units] first and last CTA of the unit
+  uint8_t* present;      // [slots] bit g: warpgroup g has a sum there
   int B, Hq, Hkv, G, Nq, Ncap;
   int units;             // units of keys of a full cache
   int row_tiles;         // of all rows of a group: ceil(G·Nq / BN)
@@ -245,6 +252,18 @@ struct KeyWIter {
   }
   __device__ __forceinline__ bool unit_ends() const { return left == 1 || s == n - 1; }
   __device__ __forceinline__ bool head_ends() const { return left == 1 || (s == n - 1 && u == seq.units - 1); }
+};
+
+// What the reading warpgroups know of a step.
+struct __align__(16) KeyWStep {
+  int rows;   // rows of the tile that count
+  int first;  // number within its head of the tile's first row
+  int least;  // least number of a row in the tile (a packed tile may go on with row 0 of the next head)
+  int need;   // number of the first row that sees the unit's first key (may be negative)
+  int slot;   // where the sums go
+  int keys;   // keys of the sequence from the unit's first on
+  int per_head;
+  int pad;
 };
 
 template <int D, bool RESIDENT>
@@ -388,10 +407,13 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
     tc_commit_w(BAR(C::B_DRAIN));
     mbar_wait_inflight(BAR(C::B_DRAIN), 0, wc, 38);
   } else if (warp < 4) {
+    KeyWStep* steps = reinterpret_cast<KeyWStep*>(smem + C::STEP_OFF);
+    int q0 = 0;  // first step of the unit here
     for (int q = 0;; ++q) {
+      const size_t unit = ((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u;
       if ((q & 1) == warp - 2) {
-        const float* src = p.lse + ((size_t)it.b * p.Hq + it.hkv * p.G) * p.Nq + it.row0(p);
-        const int rows = it.rows(p);
+        const int row0 = it.row0(p), rows = it.rows(p);
+        const float* src = p.lse + ((size_t)it.b * p.Hq + it.hkv * p.G) * p.Nq + row0;
         float v[C::BN / 32];
 #pragma unroll
         for (int c = 0; c < C::BN / 32; ++c) {
@@ -401,11 +423,31 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
             if (v[c] == INFINITY) v[c] = -INFINITY;
           }
         }
+        KeyWStep st;
+        st.rows = rows;
+        st.need = p.causal ? it.u * C::KEYS - (it.seq.len - p.Nq) : -C::KEYS;
+        st.first = 0;
+        if (st.need + C::KEYS > 1) st.first = it.packed() ? row0 % p.Nq : st.need + it.t * C::BN;
+        st.least = it.packed() && st.first + C::BN > p.Nq ? 0 : st.first;
+        st.slot = (int)unit + cta;
+        st.keys = it.seq.len - it.u * C::KEYS;
+        st.per_head = !it.packed();
         if (!mbar_wait_warp(BAR(C::B_LEMPTY + q % C::NL), ((q / C::NL) & 1) ^ 1, wc, 39)) break;
 #pragma unroll
         for (int c = 0; c < C::BN / 32; ++c) lse_s[q % C::NL * C::BN + c * 32 + lane] = v[c];
+        if (lane == 0) steps[q % C::NL] = st;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::B_LFULL + q % C::NL));
+      }
+      if (warp == 2 && lane == 0) {
+        if (it.s == 0) p.range[unit].x = cta;
+        if (it.s == it.n - 1) p.range[unit].y = cta;
+        if (it.unit_ends()) {
+          int g = 0;
+          for (int sub = q0 * C::KU; sub < (q + 1) * C::KU && g != 7; ++sub) g |= 1 << sub % C::NWG;
+          p.present[unit + cta] = (uint8_t)g;
+          q0 = q + 1;
+        }
       }
       if (it.left == 1) break;
       it.next(p);
@@ -415,121 +457,120 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
     const int mykey = quarter * 32 + lane;
     const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint64_t sl2 = f2_make(p.scale_log2, p.scale_log2);
+    const KeyWStep* steps = reinterpret_cast<const KeyWStep*>(smem + C::STEP_OFF);
+    const int n_sub = it.left * C::KU;
     float sum[C::KU];
 #pragma unroll
     for (int k = 0; k < C::KU; ++k) sum[k] = 0.f;
-    bool ok = true;
-    for (int q = 0; ok; ++q) {
-      const int key0 = it.u * C::KEYS;
-      if (it.s == 0 && warp == 4 && lane == 0)
-        p.range[((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u].x = cta;
+    int slot = -1;
+    auto flush = [&] {
+      if (slot < 0) return;
+      float* dst = p.part + ((size_t)slot * C::NWG + grp) * C::KEYS + mykey;
 #pragma unroll
       for (int k = 0; k < C::KU; ++k) {
-        const int sub = q * C::KU + k;
-        if (sub % C::NWG != grp) continue;
-        const int x = sub % C::NBUF, y = q % C::NL;
-        if (!mbar_wait_warp(BAR(C::B_LFULL + y), (q / C::NL) & 1, wc, 40) ||
-            !mbar_wait_warp(BAR(C::B_SFULL + x), (sub / C::NBUF) & 1, wc, 41)) {
-          ok = false;
-          break;
+        dst[k * 128] = sum[k];
+        sum[k] = 0.f;
+      }
+    };
+    for (int sub = grp; sub < n_sub; sub += C::NWG) {
+      const int q = sub / C::KU, k = sub % C::KU, x = sub % C::NBUF, y = q % C::NL;
+      if (!mbar_wait_warp(BAR(C::B_LFULL + y), (q / C::NL) & 1, wc, 40)) break;
+      const KeyWStep st = steps[y];
+      if (st.slot != slot) {
+        flush();
+        slot = st.slot;
+      }
+      // this key is seen from row `need` of its head on; blocks of 32 columns
+      // before c0 are seen from no key of the warp, those from f0 on from all
+      const int need = st.need + k * 128 + mykey, need0 = need - lane;
+      const bool cut = need0 - quarter * 32 + 127 > st.least;
+      int rows = k * 128 < st.keys ? st.rows : 0, c0 = 0, f0 = 0, f1 = rows & ~31;
+      if (cut) {
+        if (st.per_head) {
+          c0 = min(rows, max(0, need0 - st.first) & ~31);
+          f0 = max(0, (need0 + 31 - st.first + 31) & ~31);
+        } else {
+          f0 = C::BN;
         }
-        tc_fence_after();
-        // Row i of a head sees key j when i >= j − (len − Nq).  i: number of
-        // the tile's first row; a packed tile may go on with row 0 of the next head
-        const int off = it.seq.len - p.Nq;
-        const int last = key0 + k * 128 + 127;
-        int i = 0;
-        bool cut = p.causal && last > off;  // does the mask cut through the tile?
-        bool none = key0 + k * 128 >= it.seq.len;
-        if (cut) {
-          i = it.packed() ? it.s * C::BN % p.Nq : key0 - off + it.t * C::BN;
-          cut = last - off > (it.packed() && i + C::BN > p.Nq ? 0 : i);
-          none |= !it.packed() && last - 127 - off >= i + C::BN;
-        }
-        // columns past the tile's rows are another head's rows, whatever they hold
-        const int rows = none ? 0 : it.rows(p);
-        // this key is seen from row `need` of its head on
-        const int need = cut ? key0 + k * 128 + mykey - off : 0;
-        int c0 = 0;
-        if (cut && !it.packed()) c0 = max(0, need - lane - i) & ~31;  // blocks that no key of the warp is seen from
-        uint64_t acc[2] = {0, 0};
+      }
+      if (!mbar_wait_warp(BAR(C::B_SFULL + x), (sub / C::NBUF) & 1, wc, 41)) break;
+      tc_fence_after();
+      const uint32_t base = tl + x * C::BN;
+      const float4* ng = reinterpret_cast<const float4*>(lse_s + y * C::BN);
+      uint64_t acc[2] = {0, 0};
+      // columns [from, to) under a mask: the rest of the tile's columns are
+      // another head's rows, whatever they hold
+      auto masked = [&](int from, int to) {
+        int i = st.first + from;
+        if (!st.per_head) i %= p.Nq;
 #pragma unroll 1
-        for (; c0 < rows; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32(tl + x * C::BN + c0, r);
-          const float4* ng = reinterpret_cast<const float4*>(lse_s + y * C::BN + c0);
-          uint32_t valid = rows - c0 >= 32 ? 0xffffffffu : (1u << (rows - c0)) - 1u;
-          if (cut) {
-            if (it.packed()) {
-              // the rows' numbers within their heads start anew at Nq
-              uint32_t m = 0;
-#pragma unroll 1
-              for (int c = 0; c < 32; ++c) {
-                m |= (i >= need ? 1u : 0u) << c;
-                if (++i == p.Nq) i = 0;
-              }
-              valid &= m;
-            } else {
-              const int first = need - i - c0;
-              if (first > 0) valid &= first < 32 ? 0xffffffffu << first : 0u;
-            }
-          }
+        for (int c0 = from; c0 < to; c0 += 16) {
+          uint32_t r[16];
+          tmem_ld16(base + c0, r);
           tmem_ld_wait();
           reg_fence(r);
-          if (__all_sync(0xffffffffu, valid == 0xffffffffu)) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              const float4 g = ng[c / 4];
-              const uint64_t e0 = f2_fma(f2_make(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
-                                         f2_make(g.x, g.y));
-              const uint64_t e1 = f2_fma(f2_make(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2,
-                                         f2_make(g.z, g.w));
-              // of the pairs 0 .. 7 of 16 columns, kKeyWPoly spread evenly
-              auto exp_pair = [&](uint64_t e, int pr) -> uint64_t {
-                if ((pr * kKeyWPoly) % 8 < kKeyWPoly) return exp2_poly5(e);
-                float a, b2;
-                f2_split(e, a, b2);
-                return f2_make(ex2(a), ex2(b2));
-              };
-              acc[0] = f2_add(acc[0], exp_pair(e0, (c / 2) % 8));
-              acc[1] = f2_add(acc[1], exp_pair(e1, (c / 2 + 1) % 8));
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 g = reinterpret_cast<const float2*>(ng)[c / 2];
-              const float e0 = fmaf(__uint_as_float(r[c]), p.scale_log2, g.x);
-              const float e1 = fmaf(__uint_as_float(r[c + 1]), p.scale_log2, g.y);
-              acc[0] = f2_add(acc[0], f2_make(ex2(valid >> c & 1 ? e0 : -INFINITY),
-                                              ex2(valid >> (c + 1) & 1 ? e1 : -INFINITY)));
-            }
+          for (int c = 0; c < 16; c += 2) {
+            const float2 g = reinterpret_cast<const float2*>(ng)[(c0 + c) / 2];
+            const bool v0 = c0 + c < to && (!cut || i >= need);
+            if (++i == p.Nq) i = 0;
+            const bool v1 = c0 + c + 1 < to && (!cut || i >= need);
+            if (++i == p.Nq) i = 0;
+            const float e0 = fmaf(__uint_as_float(r[c]), p.scale_log2, g.x);
+            const float e1 = fmaf(__uint_as_float(r[c + 1]), p.scale_log2, g.y);
+            acc[0] = f2_add(acc[0], f2_make(ex2(v0 ? e0 : -INFINITY), ex2(v1 ? e1 : -INFINITY)));
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(BAR(C::B_SEMPTY + x));
-          mbar_arrive(BAR(C::B_LEMPTY + y));
-        }
-        float a, b2, c2, d2;
-        f2_split(acc[0], a, b2);
-        f2_split(acc[1], c2, d2);
-        sum[k] += (a + b2) + (c2 + d2);
-      }
-      if (!ok) break;
-      if (it.unit_ends()) {
-        const size_t unit = ((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u;
-        float* dst = p.part + ((unit + cta) * C::NWG + grp) * C::KEYS + mykey;
+      };
+      auto block = [&](const uint32_t (&r)[16], int c0) {
 #pragma unroll
-        for (int k = 0; k < C::KU; ++k) {
-          dst[k * 128] = sum[k];
-          sum[k] = 0.f;
+        for (int c = 0; c < 16; c += 4) {
+          const float4 g = ng[(c0 + c) / 4];
+          const uint64_t e0 = f2_fma(f2_make(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
+                                     f2_make(g.x, g.y));
+          const uint64_t e1 = f2_fma(f2_make(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2,
+                                     f2_make(g.z, g.w));
+          // of the pairs 0 .. 7 of 16 columns, kKeyWPoly spread evenly
+          auto exp_pair = [&](uint64_t e, int pr) -> uint64_t {
+            if ((pr * kKeyWPoly) % 8 < kKeyWPoly) return exp2_poly5(e);
+            float a, b2;
+            f2_split(e, a, b2);
+            return f2_make(ex2(a), ex2(b2));
+          };
+          acc[0] = f2_add(acc[0], exp_pair(e0, c / 2));
+          acc[1] = f2_add(acc[1], exp_pair(e1, c / 2 + 1));
         }
-        if (it.s == it.n - 1 && warp == 4 && lane == 0) p.range[unit].y = cta;
+      };
+      if (f0 < f1) {
+        uint32_t ra[16], rb[16];
+        tmem_ld16(base + f0, ra);
+#pragma unroll 1
+        for (int c = f0; c < f1; c += 32) {
+          tmem_ld_wait();
+          reg_fence(ra);
+          tmem_ld16(base + c + 16, rb);
+          block(ra, c);
+          tmem_ld_wait();
+          reg_fence(rb);
+          if (c + 32 < f1) tmem_ld16(base + c + 32, ra);
+          block(rb, c + 16);
+        }
       }
-      if (it.left == 1) break;
-      it.next(p);
+      if (c0 < min(f0, rows)) masked(c0, min(f0, rows));
+      if (max(f0, f1) < rows) masked(max(f0, f1), rows);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(BAR(C::B_SEMPTY + x));
+        mbar_arrive(BAR(C::B_LEMPTY + y));
+      }
+      float a, b2, c2, d2;
+      f2_split(acc[0], a, b2);
+      f2_split(acc[1], c2, d2);
+      if (C::KU == 1 || k == 0) sum[0] += (a + b2) + (c2 + d2);
+      else sum[C::KU - 1] += (a + b2) + (c2 + d2);
     }
+    flush();
   }
 
   tc_fence_before();
@@ -561,9 +602,12 @@ __global__ void __launch_bounds__(256) fa_key_weights_reduce_kernel(const KeyWPa
     // (within bounds also after a call that gave up)
     const int c0 = max(ctas.x, 0), c1 = min(ctas.y, p.n_ctas - 1);
     float s = 0.f;
-    for (int c = c0; c <= c1; ++c)
+    for (int c = c0; c <= c1; ++c) {
+      const int present = p.present[unit + c];
 #pragma unroll
-      for (int g = 0; g < C::NWG; ++g) s += p.part[((unit + c) * C::NWG + g) * C::KEYS + j % C::KEYS];
+      for (int g = 0; g < C::NWG; ++g)
+        if (present >> g & 1) s += p.part[((unit + c) * C::NWG + g) * C::KEYS + j % C::KEYS];
+    }
     w += s;
   }
   p.weights_out[at] = w;

@@ -1,11 +1,14 @@
 """The work list of the key-weights kernel, restated: every CTA's run of steps
 covers each visible (query row, key) pair exactly once, reads rows in bounds,
-and writes its sums to slots of its own within the workspace."""
+and writes its sums to slots of its own within the workspace.  And the kernel's
+mbarrier protocol as a randomised model (see test_barrier_protocols)."""
 
 import random
 
 import numpy as np
 import pytest
+
+from test_barrier_protocols import _Bar, _run as _drive, _waiter
 
 N_CTAS = 148
 
@@ -75,3 +78,140 @@ def test_key_weights_work_list(seed):
     Nq = Ncap if rng.random() < 0.4 else rng.randint(0, 300)
     lens = [rng.choice([rng.randint(0, Ncap), Ncap, -1]) for _ in range(B)]
     _run(B, G, Hkv, Nq, Ncap, [max(n, 0) for n in lens], rng.random() < 0.7, bn, nres)
+
+
+def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2):
+    """One CTA's run: `units` row-tile counts of consecutive units (resident: all
+    the same; `heads` splits them into kv heads).  The 4 warps of each of the 3
+    reading warpgroups are roles of their own."""
+    rnd = random.Random(seed)
+    ku = 1 if resident else 2
+    # (unit, step in unit, unit ends, head starts, head ends)
+    per_head = max(1, len(units) // heads)
+    steps = [(u, s, s == n - 1, s == 0 and u % per_head == 0, s == n - 1 and (u + 1) % per_head == 0)
+             for u, n in enumerate(units) for s in range(n)]
+    steps[-1] = (*steps[-1][:2], True, steps[-1][3], True)
+    bars = {}
+    for name, n, count in (("kf", nk, 1), ("ke", nk, 1), ("qf", nq, 1), ("qe", nq, 1), ("sf", nbuf, 1),
+                           ("se", nbuf, 4), ("lf", nl, 1), ("le", nl, 4 * ku)):
+        for i in range(n):
+            bars[f"{name}{i}"] = _Bar(count)
+    wait = _waiter(bars)
+    tma, pipe = [], []
+    kslot, qslot, sbuf, lbuf = [None] * nk, [None] * nq, [None] * nbuf, [None] * nl
+    done = {}
+
+    def tma_done(item):
+        slots, i, what, bar = item
+        slots[i] = what
+        bars[bar].arrive()
+
+    def pipe_done(item):
+        if item[0] == "commit":
+            bars[item[1]].arrive()
+            return
+        _, x, sub, k, kwhat, q, qwhat = item
+        assert kslot[k] == kwhat and qslot[q] == qwhat and sbuf[x] is None
+        sbuf[x] = sub
+
+    def producer():
+        kseq = qseq = 0
+        for i, (u, s, ends, head, _) in enumerate(steps):
+            todo = []
+            if resident and head:
+                todo += [("q", (u // per_head, t)) for t in range(units[u])]
+            if s == 0:
+                todo += [("k", (u, k)) for k in range(ku)]
+            if not resident:
+                todo.append(("q", i))
+            for kind, what in todo:
+                seq, n, slots = (kseq, nk, kslot) if kind == "k" else (qseq, nq, qslot)
+                if seq >= n:
+                    yield from wait(f"{kind}e{seq % n}", seq // n - 1)
+                tma.append((slots, seq % n, what, f"{kind}f{seq % n}"))
+                kseq, qseq = kseq + (kind == "k"), qseq + (kind == "q")
+            yield
+
+    def mma():
+        kseq = qseq = sub = 0
+        for i, (u, s, ends, head, head_ends) in enumerate(steps):
+            if resident and head:
+                for t in range(units[u]):
+                    yield from wait(f"qf{(qseq + t) % nq}", (qseq + t) // nq)
+            if s == 0:
+                for k in range(ku):
+                    yield from wait(f"kf{(kseq + k) % nk}", (kseq + k) // nk)
+            if not resident:
+                yield from wait(f"qf{qseq % nq}", qseq // nq)
+            q, qwhat = ((qseq + s) % nq, (u // per_head, s)) if resident else (qseq % nq, i)
+            for k in range(ku):
+                x = sub % nbuf
+                if sub >= nbuf:
+                    yield from wait(f"se{x}", sub // nbuf - 1)
+                pipe.append(("mma", x, sub, (kseq + k) % nk, (u, k), q, qwhat))
+                pipe.append(("commit", f"sf{x}"))
+                sub += 1
+            if not resident:
+                pipe.append(("commit", f"qe{qseq % nq}"))
+                qseq += 1
+            elif head_ends:
+                pipe.extend(("commit", f"qe{(qseq + t) % nq}") for t in range(units[u]))
+                qseq += units[u]
+            if ends:
+                pipe.extend(("commit", f"ke{(kseq + k) % nk}") for k in range(ku))
+                kseq += ku
+            yield
+
+    def filler(w):
+        for q in range(w, len(steps), 2):
+            if q >= nl:
+                yield from wait(f"le{q % nl}", q // nl - 1)
+            yield
+            lbuf[q % nl] = q
+            bars[f"lf{q % nl}"].arrive()
+
+    def reader(grp):
+        for sub in range(grp, len(steps) * ku, 3):
+            q, x = sub // ku, sub % nbuf
+            yield from wait(f"lf{q % nl}", q // nl)
+            assert lbuf[q % nl] == q
+            yield from wait(f"sf{x}", sub // nbuf)
+            assert sbuf[x] == sub
+            yield
+            assert sbuf[x] == sub and lbuf[q % nl] == q
+            done[sub] = done.get(sub, 0) + 1
+            if done[sub] == 4:
+                sbuf[x] = None
+            bars[f"se{x}"].arrive()
+            bars[f"le{q % nl}"].arrive()
+
+    gens = {"producer": producer(), "mma": mma(), "fill0": filler(0), "fill1": filler(1)}
+    gens.update({f"wg{g}w{w}": reader(g) for g in range(3) for w in range(4)})
+    _drive(gens, {"tma": (tma, tma_done), "pipe": (pipe, pipe_done)}, rnd, max_steps=2_000_000)
+    assert done == {sub: 4 for sub in range(len(steps) * ku)}
+
+
+# (resident, K slots, Q slots, TMEM buffers) of d = 64, 128, 256
+_SHAPES = [(True, 8, 4, 4), (True, 4, 2, 4), (True, 2, 2, 8), (False, 4, 8, 4), (False, 2, 4, 4), (False, 2, 2, 8)]
+
+
+def _units(resident, nq, rng):
+    if resident:
+        return [rng.randint(1, nq)] * rng.randint(1, 12)
+    return [rng.randint(1, 7) for _ in range(rng.randint(1, 8))]
+
+
+@pytest.mark.parametrize("shape", _SHAPES)
+def test_key_weights_protocol(shape):
+    resident, nk, nq, nbuf = shape
+    for seed in range(12):
+        rng = random.Random(seed)
+        _simulate(_units(resident, nq, rng), resident, nk, nq, nbuf, 6, seed)
+
+
+def test_key_weights_model_catches_a_ring_whose_readers_change():
+    # four buffers for two fillers and three readers in turn: a reader waits for
+    # a phase of a buffer whose phase before is not filled yet
+    with pytest.raises(AssertionError):
+        for seed in range(60):
+            _simulate([1] * 24, True, 4, 2, 8, 4, seed)
