@@ -32,14 +32,24 @@
 //   warps 2, 3    −LSE·log2 e of the step's rows into shared memory (−inf for
 //                 rows past Nq and rows that see no key at all: weight 0), and
 //                 what the readers have to know about the step
-//   warps 4-15    three warpgroups, a 128-key part of a step each in turn;
+//   warps 4-19    four warpgroups, a 128-key part of a step each in turn;
 //                 thread = key
+//
+// Measured (B200, 8192-token prompt, 16 heads on 4 kv heads, d = 128): 167 us.
+// The exponentials alone would take 123 us at 1.9 GHz, the product 85 us at
+// 1.63 PFLOP/s; a warpgroup computes 70 % of the time and waits for its next
+// product in most of the rest, since 512 TMEM columns hold one S buffer for
+// each of the four warpgroups and no more.  Three warpgroups with a buffer to
+// spare: 181 us.
 #pragma once
 
 #include "sm100.cuh"
 
 namespace fa {
 
+// Measured on an 8192-token prompt (16 heads, d = 128): 0, 2 and 3 of 8 by the
+// polynomial 172, 167 and 185 us (more than 2: the added instructions cost more
+// issue slots than the special-function unit gains).
 constexpr int kKeyWPoly = 2;
 
 // 2^x of two numbers on the FMA and integer pipes.  As exp2_poly, with a
@@ -69,8 +79,8 @@ __device__ __forceinline__ uint64_t exp2_poly5(uint64_t x) {
 
 template <int D, bool RESIDENT>
 struct KeyWCfg {
-  static constexpr int THREADS = 512;
-  static constexpr int NWG = 3;                     // reading warpgroups
+  static constexpr int NWG = 4;                     // reading warpgroups
+  static constexpr int THREADS = 128 * (NWG + 1);
   static constexpr int BN = D == 256 ? 64 : 128;    // query rows of a step (MMA N)
   static constexpr int KU = RESIDENT ? 1 : 2;       // 128-key tiles of a unit
   static constexpr int KEYS = 128 * KU;
@@ -84,7 +94,7 @@ struct KeyWCfg {
   // buffers of the rows' −LSE and of the steps' KeyWStep.  A wait by parity must
   // not run a phase ahead: with a multiple of 2 and of NWG, a buffer has one
   // filling warp and the same reading warpgroups every time
-  static constexpr int NL = 6;
+  static constexpr int NL = 4;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = NK * KTILE;
   static constexpr int LSE_OFF = Q_OFF + NQ * QTILE;
@@ -444,7 +454,7 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
         if (it.s == it.n - 1) p.range[unit].y = cta;
         if (it.unit_ends()) {
           int g = 0;
-          for (int sub = q0 * C::KU; sub < (q + 1) * C::KU && g != 7; ++sub) g |= 1 << sub % C::NWG;
+          for (int sub = q0 * C::KU; sub < (q + 1) * C::KU && g != (1 << C::NWG) - 1; ++sub) g |= 1 << sub % C::NWG;
           p.present[unit + cta] = (uint8_t)g;
           q0 = q + 1;
         }
@@ -522,9 +532,9 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
           }
         }
       };
-      auto block = [&](const uint32_t (&r)[16], int c0) {
+      auto block = [&](const uint32_t (&r)[32], int c0) {
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
+        for (int c = 0; c < 32; c += 4) {
           const float4 g = ng[(c0 + c) / 4];
           const uint64_t e0 = f2_fma(f2_make(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2,
                                      f2_make(g.x, g.y));
@@ -537,33 +547,36 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
             f2_split(e, a, b2);
             return f2_make(ex2(a), ex2(b2));
           };
-          acc[0] = f2_add(acc[0], exp_pair(e0, c / 2));
-          acc[1] = f2_add(acc[1], exp_pair(e1, c / 2 + 1));
+          acc[0] = f2_add(acc[0], exp_pair(e0, c / 2 % 8));
+          acc[1] = f2_add(acc[1], exp_pair(e1, c / 2 % 8 + 1));
         }
       };
-      if (f0 < f1) {
-        uint32_t ra[16], rb[16];
-        tmem_ld16(base + f0, ra);
-#pragma unroll 1
-        for (int c = f0; c < f1; c += 32) {
-          tmem_ld_wait();
-          reg_fence(ra);
-          tmem_ld16(base + c + 16, rb);
-          block(ra, c);
-          tmem_ld_wait();
-          reg_fence(rb);
-          if (c + 32 < f1) tmem_ld16(base + c + 32, ra);
-          block(rb, c + 16);
-        }
-      }
       if (c0 < min(f0, rows)) masked(c0, min(f0, rows));
       if (max(f0, f1) < rows) masked(max(f0, f1), rows);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(BAR(C::B_SEMPTY + x));
-        mbar_arrive(BAR(C::B_LEMPTY + y));
+      // the buffer is free for the next product as soon as its last 32 columns
+      // are in registers: their arithmetic covers the product's latency
+      auto release = [&](int bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(bar));
+      };
+      if (f0 < f1) {
+#pragma unroll 1
+        for (int c = f0; c < f1; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(base + c, r);
+          tmem_ld_wait();
+          reg_fence(r);
+          if (c + 32 >= f1) {
+            tc_fence_before();
+            release(C::B_SEMPTY + x);
+          }
+          block(r, c);
+        }
+      } else {
+        tc_fence_before();
+        release(C::B_SEMPTY + x);
       }
+      release(C::B_LEMPTY + y);
       float a, b2, c2, d2;
       f2_split(acc[0], a, b2);
       f2_split(acc[1], c2, d2);

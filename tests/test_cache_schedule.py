@@ -80,9 +80,9 @@ def test_key_weights_work_list(seed):
     _run(B, G, Hkv, Nq, Ncap, [max(n, 0) for n in lens], rng.random() < 0.7, bn, nres)
 
 
-def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2):
+def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2, nwg=4):
     """One CTA's run: `units` row-tile counts of consecutive units (resident: all
-    the same; `heads` splits them into kv heads).  The 4 warps of each of the 3
+    the same; `heads` splits them into kv heads).  The 4 warps of each of the `nwg`
     reading warpgroups are roles of their own."""
     rnd = random.Random(seed)
     ku = 1 if resident else 2
@@ -171,7 +171,7 @@ def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2):
             bars[f"lf{q % nl}"].arrive()
 
     def reader(grp):
-        for sub in range(grp, len(steps) * ku, 3):
+        for sub in range(grp, len(steps) * ku, nwg):
             q, x = sub // ku, sub % nbuf
             yield from wait(f"lf{q % nl}", q // nl)
             assert lbuf[q % nl] == q
@@ -186,7 +186,7 @@ def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2):
             bars[f"le{q % nl}"].arrive()
 
     gens = {"producer": producer(), "mma": mma(), "fill0": filler(0), "fill1": filler(1)}
-    gens.update({f"wg{g}w{w}": reader(g) for g in range(3) for w in range(4)})
+    gens.update({f"wg{g}w{w}": reader(g) for g in range(nwg) for w in range(4)})
     _drive(gens, {"tma": (tma, tma_done), "pipe": (pipe, pipe_done)}, rnd, max_steps=2_000_000)
     assert done == {sub: 4 for sub in range(len(steps) * ku)}
 
@@ -206,7 +206,7 @@ def test_key_weights_protocol(shape):
     resident, nk, nq, nbuf = shape
     for seed in range(12):
         rng = random.Random(seed)
-        _simulate(_units(resident, nq, rng), resident, nk, nq, nbuf, 6, seed)
+        _simulate(_units(resident, nq, rng), resident, nk, nq, nbuf, 4, seed)
 
 
 def test_key_weights_model_catches_a_ring_whose_readers_change():
@@ -214,4 +214,4 @@ def test_key_weights_model_catches_a_ring_whose_readers_change():
     # a phase of a buffer whose phase before is not filled yet
     with pytest.raises(AssertionError):
         for seed in range(60):
-            _simulate([1] * 24, True, 4, 2, 8, 4, seed)
+            _simulate([1] * 24, True, 4, 2, 8, 4, seed, nwg=3)
