@@ -11,6 +11,7 @@
 
 #include "fa.h"
 #include "fa_cache_attn.cuh"
+#include "fa_cache_tc.cuh"
 #include "fa_evict.cuh"
 #include "fa_host.h"
 #include "fa_key_weights.cuh"
@@ -71,136 +72,10 @@ fa_status cache_sizes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, f
   return FA_OK;
 }
 
-// How the keys are cut into runs: a pure function of the sizes, so that the
-// workspace sizes need no device.  Runs of equal length for the prefix and the
-// own keys, as many as give about kCacheCtas CTAs in all, but of 128 keys at
-// least (one step of each of a CTA's four warps).
-constexpr int kCacheCtas = 592;
-struct CachePlan {
-  int rg_p = 0, n_split_p = 0, kps_p = 128, rg_o = 0, n_split_o = 0, kps_o = 128;
-  size_t part_o_bytes = 0, part_ml_bytes = 0, score_bytes = 0;
-  size_t total() const { return part_o_bytes + part_ml_bytes + score_bytes; }
-};
-
-CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bool scores) {
-  CachePlan pl;
-  const long long R = (long long)(Hq / Hkv) * Nq, M = B * R;
-  pl.rg_p = (int)((M + 15) / 16);
-  pl.rg_o = (int)((R + 15) / 16);
-  const long long work = (long long)Hkv * pl.rg_p * Np + (long long)B * Hkv * pl.rg_o * Ncap;
-  const long long kps = std::max<long long>(128, ((work + kCacheCtas - 1) / kCacheCtas + 127) / 128 * 128);
-  pl.kps_p = pl.kps_o = (int)std::min<long long>(kps, 1LL << 30);
-  pl.n_split_p = (int)((Np + (long long)pl.kps_p - 1) / pl.kps_p);
-  pl.n_split_o = (int)((Ncap + (long long)pl.kps_o - 1) / pl.kps_o);
-  const size_t rows = (size_t)pl.n_split_p * Hkv * M + (size_t)pl.n_split_o * B * Hkv * R;
-  pl.part_o_bytes = round256(rows * d * 4);
-  pl.part_ml_bytes = round256(rows * 2 * 4);
-  if (scores) pl.score_bytes = round256((size_t)B * Hkv * R * ((Ncap + 31) / 32 * 32) * 4);
-  return pl;
-}
-
-template <int D>
-fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, cudaStream_t s) {
-  using C = fa::CacheCfg<D>;
-  auto kern = fa::fa_cache_split_kernel<D>;
-  static std::atomic<unsigned long long> allowed{0};
-  const fa_status st = allow_smem(kern, C::SMEM_BYTES, allowed);
-  if (st != FA_OK) return st;
-  const long long ctas = (long long)p.Hkv * p.rg_p * p.n_split_p + (long long)p.B * p.Hkv * p.rg_o * p.n_split_o;
-  if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
-  if (ctas > 0) {
-    kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p);
-    if (launched() != FA_OK) return FA_ERR_CUDA;
-  }
-  const long long rows = (long long)p.B * p.Hq * p.Nq;
-  if (rows > 0) {
-    fa::fa_cache_combine_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
-    if (launched() != FA_OK) return FA_ERR_CUDA;
-  }
-  if (p.weights_out && p.Ncap > 0) {
-    fa::fa_cache_weights_kernel<<<dim3((unsigned)((p.Ncap + 1023) / 1024), (unsigned)(p.B * p.Hkv)), 256, 0, s>>>(p);
-    return launched();
-  }
-  return FA_OK;
-}
-
-// Shared by the two decoding calls; weights_out null for the prefix form.
-fa_status cache_decode(const void* q, const void* kp, const void* vp, const void* k, const void* v,
-                       const int* lengths, const float* weights, float* weights_out, void* o, float* lse, int B,
-                       int Hq, int Hkv, int Nq, int Np, int Ncap, int d, int causal, float scale, void* workspace,
-                       size_t workspace_bytes, cudaStream_t s) {
-  const bool scores = weights_out != nullptr;
-  const CachePlan pl = cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, scores);
-  if (!workspace || (Nq > 0 && (!q || !o || !lse || (Np > 0 && (!kp || !vp)) || (Ncap > 0 && (!k || !v)))))
-    return FA_ERR_INVALID_ARG;
-  for (const void* ptr : {q, kp, vp, k, v, (const void*)o, (const void*)lse})
-    if (!aligned16(ptr)) return FA_ERR_INVALID_ARG;
-  if (!aligned4(lengths) || !aligned4(weights) || !aligned4(weights_out)) return FA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.total()) return FA_ERR_INVALID_ARG;
-  const size_t qbytes = (size_t)B * Hq * Nq * d * 2, lbytes = (size_t)B * Hq * Nq * 4;
-  const size_t kvbytes = (size_t)B * Hkv * Ncap * d * 2, pbytes = (size_t)Hkv * Np * d * 2;
-  const size_t wbytes = (size_t)B * Hkv * Ncap * 4;
-  // weights_out may be weights itself
-  const Range ins[7] = {span(q, qbytes),
-                        span(kp, pbytes),
-                        span(vp, pbytes),
-                        span(k, kvbytes),
-                        span(v, kvbytes),
-                        span(lengths, lengths ? (size_t)B * 4 : 0),
-                        span(weights, weights && weights != weights_out ? wbytes : 0)};
-  const Range outs[4] = {span(o, qbytes), span(lse, lbytes), span(workspace, pl.total()),
-                         span(weights_out, weights_out ? wbytes : 0)};
-  if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
-  DeviceInfo* di = nullptr;
-  const fa_status st = current_device(&di);
-  if (st != FA_OK) return st;
-
-  // an absent cache's maps are never read: the other's stand in
-  const int box = d == 256 ? fa::CacheCfg<256>::CH : fa::CacheCfg<128>::CH;
-  CUtensorMap maps[4] = {};
-  const uint64_t prows = (uint64_t)Hkv * Np, krows = (uint64_t)B * Hkv * Ncap;
-  if (Np > 0 && (!make_map(&maps[0], kp, prows, d, box) || !make_map(&maps[1], vp, prows, d, box))) return FA_ERR_CUDA;
-  if (Nq > 0 && Ncap > 0 && (!make_map(&maps[2], k, krows, d, box) || !make_map(&maps[3], v, krows, d, box))) return FA_ERR_CUDA;
-
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  fa::CacheParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.lengths = lengths;
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + pl.part_o_bytes);
-  p.scores = scores ? reinterpret_cast<float*>(ws + pl.part_o_bytes + pl.part_ml_bytes) : nullptr;
-  p.weights = weights;
-  p.weights_out = weights_out;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.Nq = Nq;
-  p.R = p.G * Nq;
-  p.M = B * p.R;
-  p.Np = Np;
-  p.Ncap = Ncap;
-  p.cap_pad = (Ncap + 31) / 32 * 32;
-  p.rg_p = pl.rg_p;
-  p.n_split_p = pl.n_split_p;
-  p.kps_p = pl.kps_p;
-  p.rg_o = pl.rg_o;
-  p.n_split_o = pl.n_split_o;
-  p.kps_o = pl.kps_o;
-  p.causal = causal != 0;
-  p.scale_log2 = scale * fa::kLog2e;
-  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
-  p.err = di->err;
-  switch (d) {
-    case 64: return launch_cache<64>(maps, p, s);
-    case 128: return launch_cache<128>(maps, p, s);
-    default: return launch_cache<256>(maps, p, s);
-  }
-}
-
 // ------------------------------------------------------------ key weights
+bool weights_sizes(int B, int Hkv, int Nk) {
+  return (long long)B * Hkv <= 65535 && (long long)B * Hkv * (Nk + 255LL) <= kIndexLimit;
+}
 fa_status key_weights_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, bool* empty) {
   *empty = false;
   if (B < 0 || Nq < 0 || Nk < 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return FA_ERR_INVALID_ARG;
@@ -213,7 +88,7 @@ fa_status key_weights_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float
   }
   if (B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
   if (Nq > 0 && (long long)B * Hq > kIndexLimit / Nq) return FA_ERR_UNSUPPORTED;
-  if ((long long)B * Hkv > 65535 || (long long)B * Hkv * (Nk + 255LL) > kIndexLimit) return FA_ERR_UNSUPPORTED;
+  if (!weights_sizes(B, Hkv, Nk)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
@@ -267,6 +142,211 @@ fa_status launch_key_weights(const void* q, const void* k, const fa::KeyWParams&
   return resident ? launch_key_weights<D, true>(q, k, p, s) : launch_key_weights<D, false>(q, k, p, s);
 }
 
+// The arguments are checked, the workspace is large enough.
+fa_status key_weights_run(const void* q, const void* k, const float* lse, const int* lengths, const float* weights,
+                          float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                          void* workspace, int* err, cudaStream_t s) {
+  const KeyWPlan pl = key_weights_plan(B, Hq, Hkv, Nq, Nk, d);
+  fa::KeyWParams p{};
+  p.lse = lse;
+  p.lengths = lengths;
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.part = static_cast<float*>(workspace);
+  p.range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + pl.part_bytes);
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Nq = Nq;
+  p.Ncap = Nk;
+  p.present = static_cast<uint8_t*>(workspace) + pl.part_bytes + pl.range_bytes;
+  p.units = pl.units;
+  p.row_tiles = pl.row_tiles;
+  p.n_ctas = kKeyWCtas;
+  p.causal = causal != 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
+  p.err = err;
+  switch (d) {
+    case 64: return launch_key_weights<64>(q, k, p, pl.resident, s);
+    case 128: return launch_key_weights<128>(q, k, p, pl.resident, s);
+    default: return launch_key_weights<256>(q, k, p, pl.resident, s);
+  }
+}
+
+// ------------------------------------------------------- decoding, weights
+// Up to 16 query rows against one run of keys go to fa_cache_split_kernel, whose
+// tile is 16 rows; more to fa_cache_tc_kernel.  A pure function of the sizes, so
+// that the workspace sizes need no device.
+constexpr int kWarpRows = 16;
+constexpr int kSms = 148;
+struct CachePlan {
+  bool tc_p = false, tc_o = false, scores = false, key_weights = false;
+  int units_w = 0, units_t = 0, ctas_w = 0;
+  size_t w_o = 0, w_ml = 0, w_range = 0, t_o = 0, t_ml = 0, t_range = 0, score_off = 0, keyw_off = 0, bytes = 0;
+};
+
+CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bool weights) {
+  CachePlan pl;
+  const long long R = (long long)(Hq / Hkv) * Nq, M = B * R;
+  pl.tc_p = M > kWarpRows;
+  pl.tc_o = R > kWarpRows;
+  const long long units_p = Np > 0 ? Hkv * ((M + (pl.tc_p ? 127 : 15)) / (pl.tc_p ? 128 : 16)) : 0;
+  const long long units_o = Ncap > 0 ? (long long)B * Hkv * ((R + (pl.tc_o ? 127 : 15)) / (pl.tc_o ? 128 : 16)) : 0;
+  pl.units_t = (int)((pl.tc_p ? units_p : 0) + (pl.tc_o ? units_o : 0));
+  pl.units_w = (int)((pl.tc_p ? 0 : units_p) + (pl.tc_o ? 0 : units_o));
+  pl.ctas_w = d == 64 ? 2 * kSms : kSms;  // as many as run at once
+  auto take = [&](size_t bytes) {
+    const size_t at = pl.bytes;
+    pl.bytes += round256(bytes);
+    return at;
+  };
+  if (pl.units_w > 0) {
+    const size_t rows = ((size_t)pl.units_w + pl.ctas_w) * kWarpRows;
+    pl.w_o = take(rows * d * 4);
+    pl.w_ml = take(rows * 8);
+    pl.w_range = take((size_t)pl.units_w * sizeof(int2));
+  }
+  if (pl.units_t > 0) {
+    const size_t rows = ((size_t)pl.units_t + kSms) * 128;
+    pl.t_o = take(rows * d * 4);
+    pl.t_ml = take(rows * 8);
+    pl.t_range = take((size_t)pl.units_t * sizeof(int2));
+  }
+  // up to 16 rows: their scores are kept (4 bytes a row and key) and turned into
+  // weights; more: the keys are read once more by the kernel for known LSE
+  // (2d bytes a key), which is less than keeping and reading back 16 scores
+  pl.scores = weights && !pl.tc_o;
+  pl.key_weights = weights && pl.tc_o;
+  if (pl.scores) pl.score_off = take((size_t)B * Hkv * R * ((Ncap + 31) / 32 * 32) * 4);
+  if (pl.key_weights) pl.keyw_off = take(key_weights_plan(B, Hq, Hkv, Nq, Ncap, d).total());
+  return pl;
+}
+
+template <int D>
+fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, fa::CacheList lw, fa::CacheList lt,
+                       bool tc_p, bool tc_o, cudaStream_t s) {
+  using W = fa::CacheCfg<D>;
+  using T = fa::FwdCfg<D, 1>;
+  lw.keys = W::KT;
+  if (lw.prefix_units + lw.own_rt > 0) {
+    auto kern = fa::fa_cache_split_kernel<D>;
+    static std::atomic<unsigned long long> allowed{0};
+    if (allow_smem(kern, W::SMEM_BYTES, allowed) != FA_OK) return FA_ERR_CUDA;
+    kern<<<(unsigned)lw.n_ctas, W::THREADS, W::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p, lw);
+    if (launched() != FA_OK) return FA_ERR_CUDA;
+  }
+  if (lt.prefix_units + lt.own_rt > 0) {
+    auto kern = fa::fa_cache_tc_kernel<D>;
+    static std::atomic<unsigned long long> allowed{0};
+    if (allow_smem(kern, T::SMEM_BYTES, allowed) != FA_OK) return FA_ERR_CUDA;
+    kern<<<(unsigned)lt.n_ctas, T::THREADS, T::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p, lt);
+    if (launched() != FA_OK) return FA_ERR_CUDA;
+  }
+  const unsigned combine = (unsigned)(((long long)p.B * p.Hq * p.Nq + 7) / 8);
+  const unsigned per = p.weights_out ? (unsigned)((p.Ncap + fa::kCacheWeightKeys - 1) / fa::kCacheWeightKeys) : 0;
+  const unsigned ctas = combine + (unsigned)(p.B * p.Hkv) * per;
+  if (ctas > 0) fa::fa_cache_finish_kernel<D><<<ctas, 256, 0, s>>>(p, tc_p ? lt : lw, tc_o ? lt : lw, combine);
+  return launched();
+}
+
+// Shared by the two decoding calls; weights_out null for the prefix form.
+fa_status cache_decode(const void* q, const void* kp, const void* vp, const void* k, const void* v,
+                       const int* lengths, const float* weights, float* weights_out, void* o, float* lse, int B,
+                       int Hq, int Hkv, int Nq, int Np, int Ncap, int d, int causal, float scale, void* workspace,
+                       size_t workspace_bytes, cudaStream_t s) {
+  const CachePlan pl = cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, weights_out != nullptr);
+  if (!workspace || (Nq > 0 && (!q || !o || !lse || (Np > 0 && (!kp || !vp)) || (Ncap > 0 && (!k || !v)))))
+    return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {q, kp, vp, k, v, (const void*)o, (const void*)lse})
+    if (!aligned16(ptr)) return FA_ERR_INVALID_ARG;
+  if (!aligned4(lengths) || !aligned4(weights) || !aligned4(weights_out)) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < pl.bytes) return FA_ERR_INVALID_ARG;
+  const size_t qbytes = (size_t)B * Hq * Nq * d * 2, lbytes = (size_t)B * Hq * Nq * 4;
+  const size_t kvbytes = (size_t)B * Hkv * Ncap * d * 2, pbytes = (size_t)Hkv * Np * d * 2;
+  const size_t wbytes = (size_t)B * Hkv * Ncap * 4;
+  // weights_out may be weights itself
+  const Range ins[7] = {span(q, qbytes),
+                        span(kp, pbytes),
+                        span(vp, pbytes),
+                        span(k, kvbytes),
+                        span(v, kvbytes),
+                        span(lengths, lengths ? (size_t)B * 4 : 0),
+                        span(weights, weights && weights != weights_out ? wbytes : 0)};
+  const Range outs[4] = {span(o, qbytes), span(lse, lbytes), span(workspace, pl.bytes),
+                         span(weights_out, weights_out ? wbytes : 0)};
+  if (!disjoint(ins, outs)) return FA_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  const fa_status st = current_device(&di);
+  if (st != FA_OK) return st;
+
+  // boxes: the steps of the split kernel's warps, or 128 keys; the maps of an
+  // absent cache are never read
+  const int step = d == 256 ? fa::CacheCfg<256>::CH : fa::CacheCfg<128>::CH;
+  CUtensorMap maps[4] = {};
+  const uint64_t prows = (uint64_t)Hkv * Np, krows = (uint64_t)B * Hkv * Ncap;
+  if (Nq > 0 && Np > 0)
+    for (int i = 0; i < 2; ++i)
+      if (!make_map(&maps[i], i ? vp : kp, prows, d, pl.tc_p ? 128 : step)) return FA_ERR_CUDA;
+  if (Nq > 0 && Ncap > 0)
+    for (int i = 0; i < 2; ++i)
+      if (!make_map(&maps[2 + i], i ? v : k, krows, d, pl.tc_o ? 128 : step)) return FA_ERR_CUDA;
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fa::CacheParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.lengths = lengths;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.scores = pl.scores ? reinterpret_cast<float*>(ws + pl.score_off) : nullptr;
+  p.weights = weights;
+  p.weights_out = pl.scores ? weights_out : nullptr;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.Nq = Nq;
+  p.R = p.G * Nq;
+  p.M = B * p.R;
+  p.Np = Np;
+  p.Ncap = Ncap;
+  p.cap_pad = (Ncap + 31) / 32 * 32;
+  p.causal = causal != 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
+  p.err = di->err;
+  fa::CacheList lw{}, lt{};
+  lw.rows = kWarpRows;
+  lw.n_ctas = pl.ctas_w;
+  lw.part_o = reinterpret_cast<float*>(ws + pl.w_o);
+  lw.part_ml = reinterpret_cast<float*>(ws + pl.w_ml);
+  lw.range = reinterpret_cast<int2*>(ws + pl.w_range);
+  lt.rows = lt.keys = 128;
+  lt.n_ctas = kSms;
+  lt.part_o = reinterpret_cast<float*>(ws + pl.t_o);
+  lt.part_ml = reinterpret_cast<float*>(ws + pl.t_ml);
+  lt.range = reinterpret_cast<int2*>(ws + pl.t_range);
+  if (p.M > 0 && Np > 0) {
+    fa::CacheList& l = pl.tc_p ? lt : lw;
+    l.prefix_rt = (p.M + l.rows - 1) / l.rows;
+    l.prefix_units = Hkv * l.prefix_rt;
+  }
+  if (p.R > 0 && Ncap > 0) {
+    fa::CacheList& l = pl.tc_o ? lt : lw;
+    l.own_rt = (p.R + l.rows - 1) / l.rows;
+  }
+  fa_status res;
+  switch (d) {
+    case 64: res = launch_cache<64>(maps, p, lw, lt, pl.tc_p, pl.tc_o, s); break;
+    case 128: res = launch_cache<128>(maps, p, lw, lt, pl.tc_p, pl.tc_o, s); break;
+    default: res = launch_cache<256>(maps, p, lw, lt, pl.tc_p, pl.tc_o, s); break;
+  }
+  if (res != FA_OK || !pl.key_weights || Ncap == 0) return res;
+  return key_weights_run(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Ncap, d, causal, scale,
+                         ws + pl.keyw_off, di->err, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -274,7 +354,7 @@ extern "C" {
 size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d) {
   bool empty = false;
   if (cache_sizes(B, Hq, Hkv, Nq, Np, Ncap, d, 1.f, &empty) != FA_OK) return 0;
-  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, false).total());
+  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, false).bytes);
 }
 
 fa_status fa_fwd_decode_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
@@ -291,8 +371,8 @@ fa_status fa_fwd_decode_prefix(const void* q, const void* k_prefix, const void* 
 size_t fa_decode_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
   bool empty = false;
   if (cache_sizes(B, Hq, Hkv, Nq, 0, Nk, d, 1.f, &empty) != FA_OK) return 0;
-  if ((long long)B * Hkv > 65535) return 0;
-  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, 0, Nk, d, true).total());
+  if (!weights_sizes(B, Hkv, Nk)) return 0;
+  return empty ? 256 : std::max<size_t>(256, cache_plan(B, Hq, Hkv, Nq, 0, Nk, d, true).bytes);
 }
 
 fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, const int* lengths, const float* weights,
@@ -301,7 +381,7 @@ fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, con
   bool empty = false;
   const fa_status st = cache_sizes(B, Hq, Hkv, Nq, 0, Nk, d, scale, &empty);
   if (st != FA_OK || B == 0 || (Nq == 0 && Nk == 0)) return st;
-  if ((long long)B * Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (!weights_sizes(B, Hkv, Nk)) return FA_ERR_UNSUPPORTED;
   if (Nk > 0 && !weights_out) return FA_ERR_INVALID_ARG;
   return cache_decode(q, nullptr, nullptr, k, v, lengths, weights, weights_out, o, lse, B, Hq, Hkv, Nq, 0, Nk, d,
                       causal, scale, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
@@ -335,33 +415,8 @@ fa_status fa_key_weights(const void* q, const void* k, const float* lse, const i
   DeviceInfo* di = nullptr;
   st = current_device(&di);
   if (st != FA_OK) return st;
-  fa::KeyWParams p{};
-  p.lse = lse;
-  p.lengths = lengths;
-  p.weights = weights;
-  p.weights_out = weights_out;
-  p.part = static_cast<float*>(workspace);
-  p.range = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + pl.part_bytes);
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.Nq = Nq;
-  p.Ncap = Nk;
-  p.present = static_cast<uint8_t*>(workspace) + pl.part_bytes + pl.range_bytes;
-  p.units = pl.units;
-  p.row_tiles = pl.row_tiles;
-  p.n_ctas = kKeyWCtas;
-  p.causal = causal != 0;
-  p.scale_log2 = scale * fa::kLog2e;
-  p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);
-  p.err = di->err;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  switch (d) {
-    case 64: return launch_key_weights<64>(q, k, p, pl.resident, s);
-    case 128: return launch_key_weights<128>(q, k, p, pl.resident, s);
-    default: return launch_key_weights<256>(q, k, p, pl.resident, s);
-  }
+  return key_weights_run(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale, workspace, di->err,
+                         static_cast<cudaStream_t>(stream));
 }
 
 fa_status fa_cache_evict(const void* k, const void* v, const float* weights, const int* lengths, void* k_out,

@@ -1,20 +1,9 @@
-// Attention of a few query rows against ragged key/value caches, with or
-// without a prefix that the whole batch shares.
+// Cache attention for up to 16 query rows against one run of keys, and the
+// joining of all partial results.
 //
-// Sequence b is the prefix (Np keys, the same for every b) followed by its own
-// n_b = lengths[b] keys out of a cache with room for Ncap.  Query row i of Nq
-// is position L_b − Nq + i of the L_b = Np + n_b long sequence:
-//   S_j = s·q·k_j,  O = Σ_j 2^(S_j' − M) v_j / Σ_j 2^(S_j' − M)   (S' = S·log2 e)
-// and the softmax over the concatenation is put together from parts: the keys
-// are cut into runs ("splits"), each run gives its running maximum m, its
-// normaliser l = Σ 2^(S' − m) and its unnormalised O, and
-//   O = Σ_r 2^(m_r − M) O_r / Σ_r 2^(m_r − M) l_r.
-// A run of the prefix serves the rows of ALL sequences (M = B·G·Nq rows of a kv
-// head), a run of own keys the R = G·Nq rows of its sequence.
-//
-//   fa_cache_split_kernel    one CTA per (run, kv head, group of 16 rows)
-//   fa_cache_combine_kernel  one warp per query row
-//   fa_cache_weights_kernel  w[j] += Σ_r 2^(S'_rj − LSE'_r) from stored scores
+//   fa_cache_split_kernel    the work list of fa_cache_list.cuh, 16-row tiles
+//   fa_cache_finish_kernel   O and LSE, one warp per query row; and
+//                            w[j] += Σ_r 2^(S'_rj − LSE'_r) from stored scores
 //
 // The split kernel is bound by reading K and V.  Its rows fill one m16n8k16
 // tile, so each warp works alone on runs of CH keys: TMA loads of its own ring
@@ -24,7 +13,7 @@
 // weights; the second product's extra instructions fit under the loads.
 #pragma once
 
-#include "sm100.cuh"
+#include "fa_cache_list.cuh"
 
 namespace fa {
 
@@ -52,38 +41,12 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // rescaled: P stays below 2^8, and no sum comes near the fp32 range
 constexpr float kCacheTau = 8.0f;
 
-struct CacheParams {
-  const __nv_bfloat16* q;  // [B, Hq, Nq, d]
-  const int* lengths;      // [B], or null: every own cache is full
-  __nv_bfloat16* o;        // [B, Hq, Nq, d]
-  float* lse;              // [B, Hq, Nq]
-  float* part_o;           // partial results: n_split_p·Hkv·M rows of the prefix, then n_split_o·B·Hkv·R own rows
-  float* part_ml;          // the same rows: m (log2 units), l
-  float* scores;           // [B·Hkv][R][cap_pad] scores in log2 units, or null
-  const float* weights;    // [B, Hkv, Ncap] or null
-  float* weights_out;
-  int B, Hq, Hkv, G, Nq, R, M;       // R = G·Nq, M = B·R
-  int Np, Ncap, cap_pad;             // cap_pad: Ncap rounded up to 32
-  int rg_p, n_split_p, kps_p;        // prefix: row groups, splits, keys per split
-  int rg_o, n_split_o, kps_o;        // own keys
-  int causal;
-  float scale_log2;
-  long long wait_cap;
-  int* err;
-};
-
-// Number of own keys of sequence b; −1 where lengths[b] breaks its rule.
-__device__ __forceinline__ int cache_len(const CacheParams& p, int b) {
-  if (!p.lengths) return p.Ncap;
-  const int n = p.lengths[b];
-  return (n < 0 || n > p.Ncap) ? -1 : n;
-}
-
 template <int D>
 struct CacheCfg {
   static constexpr int W = 4;                    // warps
   static constexpr int THREADS = W * 32;
   static constexpr int CH = D == 256 ? 16 : 32;  // keys of one warp's step
+  static constexpr int KT = W * CH;              // keys of a key tile
   static constexpr int ST = 3;                   // stages of each warp's ring
   static constexpr int PANEL = CH * 128;         // 64 columns x CH keys (bytes)
   static constexpr int TILE = PANEL * (D / 64);  // CH keys of K or V
@@ -101,42 +64,11 @@ template <int D>
 __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
     fa_cache_split_kernel(const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                          const CacheParams p) {
+                          const CacheParams p, const CacheList list) {
   using C = CacheCfg<D>;
-  // which run of keys, which rows
-  const int n_prefix = p.Hkv * p.rg_p * p.n_split_p;
-  const bool prefix = (int)blockIdx.x < n_prefix;
-  int split, rg, hkv, b, len, rows_total, key_base;
-  if (prefix) {
-    int u = blockIdx.x;
-    rg = u % p.rg_p;
-    u /= p.rg_p;
-    split = u % p.n_split_p;
-    hkv = u / p.n_split_p;
-    b = 0;
-    len = p.Np;
-    rows_total = p.M;
-    key_base = hkv * p.Np;
-  } else {
-    int u = blockIdx.x - n_prefix;
-    rg = u % p.rg_o;
-    u /= p.rg_o;
-    split = u % p.n_split_o;
-    u /= p.n_split_o;
-    hkv = u % p.Hkv;
-    b = u / p.Hkv;
-    len = cache_len(p, b);
-    rows_total = p.R;
-    key_base = (b * p.Hkv + hkv) * p.Ncap;
-    if (len < 0) {  // a length out of range: nothing of this sequence is computed
-      if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
-      return;
-    }
-  }
-  const int kps = prefix ? p.kps_p : p.kps_o;
-  const int k0 = split * kps;
-  const int k1 = min(len, k0 + kps);
-  if (k0 >= k1) return;  // past the sequence's end; the combine kernel knows
+  CacheRuns run;
+  const int cta = blockIdx.x;
+  if (!run.start(p, list, cta)) return;  // the same for every warp
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -149,46 +81,46 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
     fence_mbar_init();
   }
   __syncthreads();
-
-  const CUtensorMap* mk = prefix ? &tmKp : &tmK;
-  const CUtensorMap* mv = prefix ? &tmVp : &tmV;
-  const int n_chunks = (k1 - k0 + C::CH - 1) / C::CH;
-  const int n_mine = (n_chunks - warp + C::W - 1) / C::W;
   const uint32_t ring = sbase + warp * C::ST * C::STAGE;
   const uint32_t bars = sbase + C::BAR_OFF + warp * C::ST * 8;
+  const WaitCtx wc{abort_flag, p.err, p.wait_cap};
+  int step0 = 0;  // steps of this warp before the run: they number the ring's stages
+  while (true) {
+  const int rows_total = run.prefix ? p.M : p.R;
+  const int len = run.len;
+  // this warp's steps: key tile t0 + i, keys warp·CH .. of it
+  int n_mine = run.t1 - run.t0;
+  if ((run.t1 - 1) * C::KT + warp * C::CH >= len) --n_mine;
+  const CUtensorMap* mk = run.prefix ? &tmKp : &tmK;
+  const CUtensorMap* mv = run.prefix ? &tmVp : &tmV;
+  const int key_base = run.prefix ? run.hkv * p.Np : (run.b * p.Hkv + run.hkv) * p.Ncap;
+  auto key_of = [&](int i) { return (run.t0 + i) * C::KT + warp * C::CH; };
   auto issue = [&](int i) {
-    const int st = i % C::ST;
-    const int key0 = k0 + (warp + C::W * i) * C::CH;
+    const int st = (step0 + i) % C::ST;
     mbar_expect_tx(bars + 8 * st, C::STAGE);
 #pragma unroll
     for (int pn = 0; pn < D / 64; ++pn) {
-      tma_load_2d(ring + st * C::STAGE + pn * C::PANEL, mk, bars + 8 * st, pn * 64, key_base + key0);
-      tma_load_2d(ring + st * C::STAGE + C::TILE + pn * C::PANEL, mv, bars + 8 * st, pn * 64, key_base + key0);
+      tma_load_2d(ring + st * C::STAGE + pn * C::PANEL, mk, bars + 8 * st, pn * 64, key_base + key_of(i));
+      tma_load_2d(ring + st * C::STAGE + C::TILE + pn * C::PANEL, mv, bars + 8 * st, pn * 64, key_base + key_of(i));
     }
   };
   if (lane == 0)
     for (int i = 0; i < C::ST && i < n_mine; ++i) issue(i);
+  if (threadIdx.x == 0) run.note(list, cta);
 
   // this lane's two query rows: first operand fragments and last visible key
-  const int row0 = rg * 16 + (lane >> 2);
+  const int row0 = run.rt * 16 + (lane >> 2);
   uint32_t qf[D / 16][4];
   int last[2];
   size_t score_row[2] = {0, 0};
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int m = row0 + 8 * x;
-    last[x] = -1;
+    last[x] = cache_last(p, run.prefix, run.b, len, m);
     const uint32_t* src = nullptr;
     if (m < rows_total) {
-      const int bb = prefix ? m / p.R : b;
-      const int r = prefix ? m - bb * p.R : m;
-      const int g = r / p.Nq, i = r - g * p.Nq;
-      src = reinterpret_cast<const uint32_t*>(p.q + ((size_t)(bb * p.Hq + hkv * p.G + g) * p.Nq + i) * D) + (lane & 3);
-      const int nb = prefix ? cache_len(p, bb) : len;
-      last[x] = len - 1;
-      if (nb < 0) last[x] = -1;
-      else if (p.causal) last[x] = (int)min((long long)len - 1, (long long)nb - p.Nq + i + (prefix ? p.Np : 0));
-      score_row[x] = ((size_t)(b * p.Hkv + hkv) * p.R + r) * p.cap_pad;
+      src = reinterpret_cast<const uint32_t*>(p.q + cache_row(p, run.prefix, run.b, run.hkv, m) * D) + (lane & 3);
+      score_row[x] = ((size_t)(run.b * p.Hkv + run.hkv) * p.R + m) * p.cap_pad;
     }
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
@@ -197,7 +129,6 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
     }
   }
 
-  const WaitCtx wc{abort_flag, p.err, p.wait_cap};
   float o[D / 8][4];
 #pragma unroll
   for (int n = 0; n < D / 8; ++n)
@@ -207,10 +138,10 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
   bool ok = true;
   int done = 0;
   for (int i = 0; i < n_mine; ++i) {
-    const int st = i % C::ST;
-    if (!mbar_wait_warp(bars + 8 * st, (i / C::ST) & 1, wc, 21)) { ok = false; break; }
+    const int st = (step0 + i) % C::ST;
+    if (!mbar_wait_warp(bars + 8 * st, ((step0 + i) / C::ST) & 1, wc, 21)) { ok = false; break; }
     done = i + 1;
-    const int key0 = k0 + (warp + C::W * i) * C::CH;
+    const int key0 = key_of(i);
     const uint32_t kt = ring + st * C::STAGE, vt = kt + C::TILE;
     if (key0 + C::CH > len) {
       // what lies behind the last key may be anything, NaN too: its weight is
@@ -249,7 +180,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
         s[nt][e] = key > last[e >> 1] ? -INFINITY : s[nt][e] * p.scale_log2;
         mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
       }
-    if (p.scores && !prefix) {
+    if (p.scores && !run.prefix) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (row0 + 8 * x < rows_total)
@@ -315,7 +246,8 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
   // a warp that gave up waits for its own copies in flight
   if (!ok && lane == 0)
     for (int i = done; i < n_mine && i < done + C::ST; ++i)
-      mbar_wait_inflight(bars + 8 * (i % C::ST), (i / C::ST) & 1, wc, 22);
+      mbar_wait_inflight(bars + 8 * ((step0 + i) % C::ST), ((step0 + i) / C::ST) & 1, wc, 22);
+  step0 += n_mine;
 
   // merge the warps: m, l and O of every row through shared memory
   float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
@@ -337,11 +269,9 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
       *reinterpret_cast<float2*>(red + ((size_t)warp * 16 + (lane >> 2) + 8 * x) * D + n * 8 + 2 * (lane & 3)) =
           make_float2(o[n][2 * x], o[n][2 * x + 1]);
   __syncthreads();
-  if (*abort_flag) return;
-  const int rows = min(16, rows_total - rg * 16);
-  const size_t slot0 = prefix ? ((size_t)split * p.Hkv + hkv) * p.M + rg * 16
-                              : (size_t)p.n_split_p * p.Hkv * p.M +
-                                    (((size_t)split * p.B + b) * p.Hkv + hkv) * p.R + rg * 16;
+  if (*abort_flag) return;  // set before the last barrier or never: the same for all
+  const int rows = min(16, rows_total - run.rt * 16);
+  const size_t slot0 = (size_t)(run.unit + cta) * 16;
   for (int e = threadIdx.x; e < rows * (D / 4); e += C::THREADS) {
     const int r = e / (D / 4), c = e - r * (D / 4);
     float M = -INFINITY;
@@ -360,27 +290,56 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
       sum.z = fmaf(f, v.z, sum.z);
       sum.w = fmaf(f, v.w, sum.w);
     }
-    reinterpret_cast<float4*>(p.part_o + (slot0 + r) * D)[c] = sum;
-    if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (slot0 + r) * 2) = make_float2(M, L);
+    reinterpret_cast<float4*>(list.part_o + (slot0 + r) * D)[c] = sum;
+    if (c == 0) *reinterpret_cast<float2*>(list.part_ml + (slot0 + r) * 2) = make_float2(M, L);
+  }
+  if (!run.next(p, list)) return;
+  fence_proxy_async_smem();  // the next run's loads overwrite what was written here
+  __syncthreads();
   }
 }
 
-// Where the partial results of one query row lie, and how many there are.
+// Where the partial results of one query row lie, and how many there are: a
+// run of consecutive slots for the prefix and one for the own keys.
 struct CacheParts {
-  size_t prefix0, prefix_step, own0, own_step;
+  struct Run {
+    const float *o, *ml;
+    size_t row;  // first row of the arrays
+    int step;    // rows from one CTA's slot to the next
+    __device__ __forceinline__ int set(const CacheList& l, int unit, int m) {
+      const int2 ctas = l.range[unit];
+      // (within bounds also after a call that gave up)
+      const int c0 = min(max(ctas.x, 0), l.n_ctas - 1), c1 = min(ctas.y, l.n_ctas - 1);
+      o = l.part_o;
+      ml = l.part_ml;
+      row = (size_t)(unit + c0) * l.rows + m % l.rows;
+      step = l.rows;
+      return max(0, c1 - c0 + 1);
+    }
+  };
+  Run prefix, own;
   int n_prefix, n;
-  __device__ size_t slot(int s) const {
-    return s < n_prefix ? prefix0 + s * prefix_step : own0 + (size_t)(s - n_prefix) * own_step;
+  __device__ __forceinline__ const float* o(int s, int d) const {
+    return s < n_prefix ? prefix.o + (prefix.row + (size_t)s * prefix.step) * d
+                        : own.o + (own.row + (size_t)(s - n_prefix) * own.step) * d;
+  }
+  __device__ __forceinline__ float2 ml(int s) const {
+    return *reinterpret_cast<const float2*>(
+        s < n_prefix ? prefix.ml + (prefix.row + (size_t)s * prefix.step) * 2
+                     : own.ml + (own.row + (size_t)(s - n_prefix) * own.step) * 2);
   }
 };
-__device__ __forceinline__ CacheParts cache_parts(const CacheParams& p, int b, int hkv, int r, int len) {
+// Row r of the R rows of sequence b's kv head.
+__device__ __forceinline__ CacheParts cache_parts(const CacheParams& p, const CacheList& lp, const CacheList& lo, int b,
+                                                  int hkv, int r, int len) {
   CacheParts c;
-  c.prefix0 = (size_t)hkv * p.M + (size_t)b * p.R + r;
-  c.prefix_step = (size_t)p.Hkv * p.M;
-  c.own0 = (size_t)p.n_split_p * p.Hkv * p.M + ((size_t)b * p.Hkv + hkv) * p.R + r;
-  c.own_step = (size_t)p.B * p.Hkv * p.R;
-  c.n_prefix = p.n_split_p;
-  c.n = p.n_split_p + (len + p.kps_o - 1) / p.kps_o;
+  c.n_prefix = 0;
+  if (p.Np > 0) {
+    const int m = b * p.R + r;
+    c.n_prefix = c.prefix.set(lp, hkv * lp.prefix_rt + m / lp.rows, m);
+  }
+  c.n = c.n_prefix;
+  if (len > 0) c.n += c.own.set(lo, lo.prefix_units + (b * p.Hkv + hkv) * lo.own_rt + r / lo.rows, r);
   return c;
 }
 
@@ -400,96 +359,107 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// O and LSE of one query row a warp.  A row that no key is visible to has
-// O = 0 and LSE = −inf.
-template <int D>
-__global__ void __launch_bounds__(256) fa_cache_combine_kernel(const CacheParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)p.B * p.Hq * p.Nq) return;
-  const int i = (int)(row % p.Nq);
-  const int h = (int)(row / p.Nq % p.Hq);
-  const int b = (int)(row / ((long long)p.Nq * p.Hq));
-  const int len = cache_len(p, b);
-  if (len < 0) {
-    if (lane == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
-    return;
-  }
-  const CacheParts parts = cache_parts(p, b, h / p.G, (h % p.G) * p.Nq + i, len);
-  float M = -INFINITY;
-  for (int s = lane; s < parts.n; s += 32) M = fmaxf(M, p.part_ml[parts.slot(s) * 2]);
+// Largest m and the sum of l on its scale over a row's partial results.
+__device__ __forceinline__ void cache_ml(const CacheParts& parts, int lane, float& M, float& L) {
+  M = -INFINITY;
+  L = 0.f;
+  for (int s = lane; s < parts.n; s += 32) M = fmaxf(M, parts.ml(s).x);
   M = warp_max(M);
-  constexpr int V = D / 32;  // columns of a lane
-  float acc[V], L = 0.f;
-#pragma unroll
-  for (int c = 0; c < V; ++c) acc[c] = 0.f;
-  for (int s0 = 0; s0 < parts.n; s0 += 32) {
-    float f = 0.f;
-    if (s0 + lane < parts.n) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + parts.slot(s0 + lane) * 2);
-      if (ml.x != -INFINITY) f = ex2(ml.x - M);
-      L = fmaf(f, ml.y, L);
-    }
-    const int cnt = min(32, parts.n - s0);
-#pragma unroll 4
-    for (int t = 0; t < cnt; ++t) {
-      const float ft = __shfl_sync(0xffffffffu, f, t);
-      const float* src = p.part_o + parts.slot(s0 + t) * D + lane * V;
-#pragma unroll
-      for (int c = 0; c < V; ++c) acc[c] = fmaf(ft, src[c], acc[c]);
-    }
+  for (int s = lane; s < parts.n; s += 32) {
+    const float2 ml = parts.ml(s);
+    if (ml.x != -INFINITY) L = fmaf(ex2(ml.x - M), ml.y, L);
   }
   L = warp_sum(L);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (size_t)row * D + lane * V);
-#pragma unroll
-  for (int c = 0; c < V; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
-  if (lane == 0) p.lse[row] = L > 0.f ? (M + lg2(L)) * kLn2 : -INFINITY;
 }
 
-// weights_out[j] = weights[j] + Σ_r 2^(S'_rj − LSE'_r); keys at or behind the
-// sequence's length keep their weight.  One CTA per (sequence, kv head, 1024
-// keys), rows taken 64 at a time.
-__global__ void __launch_bounds__(256) fa_cache_weights_kernel(const CacheParams p) {
-  __shared__ float lse2[64];
-  const int unit = blockIdx.y, b = unit / p.Hkv, hkv = unit % p.Hkv;
+// Keys of a CTA of the weights' part of the finish kernel.
+constexpr int kCacheWeightKeys = 1024;
+
+// CTAs 0 .. n_combine−1: O and LSE, one query row a warp; a row that no key is
+// visible to has O = 0 and LSE = −inf.  The CTAs behind them (only with stored
+// scores, R <= 16): weights_out[j] = weights[j] + Σ_r 2^(S'_rj − LSE'_r), one CTA
+// for kCacheWeightKeys keys of a (sequence, kv head); keys at or behind the
+// sequence's length keep their weight.  Each joins the rows' m and l by itself
+// rather than wait for the others' LSE in a launch of its own.
+template <int D>
+__global__ void __launch_bounds__(256)
+    fa_cache_finish_kernel(const CacheParams p, const CacheList lp, const CacheList lo, unsigned n_combine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x < n_combine) {
+    const long long row = (long long)blockIdx.x * 8 + warp;
+    if (row >= (long long)p.B * p.Hq * p.Nq) return;
+    const int i = (int)(row % p.Nq);
+    const int h = (int)(row / p.Nq % p.Hq);
+    const int b = (int)(row / ((long long)p.Nq * p.Hq));
+    const int len = cache_len(p, b);
+    if (len < 0) {
+      if (lane == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
+      return;
+    }
+    const CacheParts parts = cache_parts(p, lp, lo, b, h / p.G, (h % p.G) * p.Nq + i, len);
+    float M, L;
+    cache_ml(parts, lane, M, L);
+    constexpr int V = D / 32;  // columns of a lane
+    float acc[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) acc[c] = 0.f;
+    for (int s0 = 0; s0 < parts.n; s0 += 32) {
+      float f = 0.f;
+      if (s0 + lane < parts.n) {
+        const float m = parts.ml(s0 + lane).x;
+        if (m != -INFINITY) f = ex2(m - M);
+      }
+      const int cnt = min(32, parts.n - s0);
+#pragma unroll 4
+      for (int t = 0; t < cnt; ++t) {
+        const float ft = __shfl_sync(0xffffffffu, f, t);
+        const float* src = parts.o(s0 + t, D) + lane * V;
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(ft, src[c], acc[c]);
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + (size_t)row * D + lane * V);
+#pragma unroll
+    for (int c = 0; c < V; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+    if (lane == 0) p.lse[row] = L > 0.f ? (M + lg2(L)) * kLn2 : -INFINITY;
+    return;
+  }
+
+  __shared__ float lse2[16];
+  const int per = (p.Ncap + kCacheWeightKeys - 1) / kCacheWeightKeys;
+  const int unit = (blockIdx.x - n_combine) / per, b = unit / p.Hkv;
+  const int j = (blockIdx.x - n_combine) % per * kCacheWeightKeys + 4 * (int)threadIdx.x;
   const int len = cache_len(p, b);
   if (len < 0) {  // this sequence's weights stay as they are
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
     return;
   }
-  const int j0 = blockIdx.x * 1024;
+  for (int r = warp; r < p.R; r += 8) {
+    float M, L;
+    cache_ml(cache_parts(p, lp, lo, b, unit % p.Hkv, r, len), lane, M, L);
+    // a row without a visible key gives no weight (its scores are −inf)
+    if (lane == 0) lse2[r] = L > 0.f ? M + lg2(L) : INFINITY;
+  }
+  __syncthreads();
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int r0 = 0; r0 < p.R && j0 < len; r0 += 64) {
-    __syncthreads();
-    for (int r = r0 + (threadIdx.x >> 5); r < min(p.R, r0 + 64); r += 8) {
-      const int lane = threadIdx.x & 31;
-      const CacheParts parts = cache_parts(p, b, hkv, r, len);
-      float M = -INFINITY, L = 0.f;
-      for (int s = lane; s < parts.n; s += 32) M = fmaxf(M, p.part_ml[parts.slot(s) * 2]);
-      M = warp_max(M);
-      for (int s = lane; s < parts.n; s += 32) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + parts.slot(s) * 2);
-        if (ml.x != -INFINITY) L = fmaf(ex2(ml.x - M), ml.y, L);
-      }
-      L = warp_sum(L);
-      // a row without a visible key gives no weight (its scores are −inf)
-      if (lane == 0) lse2[r - r0] = L > 0.f ? M + lg2(L) : INFINITY;
+  if (j < len) {  // scores are stored up to a multiple of 32 keys
+    const float* src = p.scores + (size_t)unit * p.R * p.cap_pad + j;
+#pragma unroll 4
+    for (int r = 0; r < p.R; ++r) {
+      const float4 s = *reinterpret_cast<const float4*>(src + (size_t)r * p.cap_pad);
+      acc[0] += ex2(s.x - lse2[r]);
+      acc[1] += ex2(s.y - lse2[r]);
+      acc[2] += ex2(s.z - lse2[r]);
+      acc[3] += ex2(s.w - lse2[r]);
     }
-    __syncthreads();
-    const float* src = p.scores + ((size_t)unit * p.R + r0) * p.cap_pad + j0 + threadIdx.x;
-    for (int r = 0; r < min(64, p.R - r0); ++r)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (j0 + threadIdx.x + 256 * t < len) acc[t] += ex2(src[(size_t)r * p.cap_pad + 256 * t] - lse2[r]);
   }
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int j = j0 + threadIdx.x + 256 * t;
-    if (j >= p.Ncap) continue;
-    const size_t at = (size_t)unit * p.Ncap + j;
+    if (j + t >= p.Ncap) continue;
+    const size_t at = (size_t)unit * p.Ncap + j + t;
     const float w = p.weights ? p.weights[at] : 0.f;
-    p.weights_out[at] = j < len ? w + acc[t] : w;
+    p.weights_out[at] = j + t < len ? w + acc[t] : w;
   }
 }
 

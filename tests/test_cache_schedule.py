@@ -1,7 +1,8 @@
-"""The work list of the key-weights kernel, restated: every CTA's run of steps
-covers each visible (query row, key) pair exactly once, reads rows in bounds,
-and writes its sums to slots of its own within the workspace.  And the kernel's
-mbarrier protocol as a randomised model (see test_barrier_protocols)."""
+"""The work lists of the cache kernels, restated: the CTAs' runs cover each
+visible (query row, key) pair of the key weights, and each key tile of the cache
+attention, exactly once, read rows in bounds, and write to slots of their own
+within the workspace.  And the mbarrier protocol of the key-weights kernel as a
+randomised model (see test_barrier_protocols)."""
 
 import random
 
@@ -78,6 +79,86 @@ def test_key_weights_work_list(seed):
     Nq = Ncap if rng.random() < 0.4 else rng.randint(0, 300)
     lens = [rng.choice([rng.randint(0, Ncap), Ncap, -1]) for _ in range(B)]
     _run(B, G, Hkv, Nq, Ncap, [max(n, 0) for n in lens], rng.random() < 0.7, bn, nres)
+
+
+def _cache_runs(p_units, p_rt, np_keys, Hkv, own_rt, lens, keys, n_ctas, cta):
+    """CacheRuns restated: yields (unit, prefix, b, hkv, rt, t0, t1, tiles)."""
+    tiles_of = lambda n: -(-n // keys) if n > 0 else 0  # noqa: E731
+    in_prefix = p_units * tiles_of(np_keys)
+    own = [Hkv * own_rt * tiles_of(n) for n in lens]
+    total = in_prefix + sum(own)
+    per = -(-total // n_ctas)
+    x = per * cta
+    if x >= total:
+        return
+    left = min(total, x + per) - x
+    if x < in_prefix:
+        prefix, tiles = True, tiles_of(np_keys)
+        unit, t0 = divmod(x, tiles)
+        b, (hkv, rt) = 0, divmod(unit, p_rt)
+    else:
+        x -= in_prefix
+        prefix, b = False, 0
+        while x >= own[b]:
+            x -= own[b]
+            b += 1
+        tiles = tiles_of(lens[b])
+        u, t0 = divmod(x, tiles)
+        hkv, rt = divmod(u, own_rt)
+        unit = p_units + (b * Hkv + hkv) * own_rt + rt
+    while True:
+        t1 = min(tiles, t0 + left)
+        yield unit, prefix, b, hkv, rt, t0, t1, tiles
+        left -= t1 - t0
+        if left <= 0:
+            return
+        t0 = 0
+        if prefix and unit + 1 < p_units:
+            unit += 1
+            hkv, rt = divmod(unit, p_rt)
+            continue
+        if prefix:
+            prefix, b, hkv, rt = False, -1, Hkv - 1, own_rt - 1
+        rt += 1
+        if rt == own_rt:
+            rt, hkv = 0, hkv + 1
+            if hkv == Hkv:
+                hkv, b = 0, b + 1
+                while tiles_of(lens[b]) == 0:
+                    b += 1
+                tiles = tiles_of(lens[b])
+        unit = p_units + (b * Hkv + hkv) * own_rt + rt
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_cache_work_list(seed):
+    rng = random.Random(seed)
+    keys, n_ctas = rng.choice([(128, 148), (64, 148), (128, 296)])
+    B, Hkv, own_rt = rng.randint(1, 40), rng.randint(1, 4), rng.choice([0, 1, 1, 2])
+    p_rt = rng.choice([0, 1, 3]) if own_rt else 1
+    np_keys = rng.choice([rng.randint(1, 300), rng.randint(1, 30000)])
+    lens = [rng.choice([0, -1, rng.randint(0, 400), rng.randint(0, 5000)]) for _ in range(B)] if own_rt else [0] * B
+    p_units, seen, slots, ranges = Hkv * p_rt, {}, {}, {}
+    for cta in range(n_ctas):
+        for unit, prefix, b, hkv, rt, t0, t1, tiles in _cache_runs(p_units, p_rt, np_keys, Hkv, own_rt, lens, keys,
+                                                                 n_ctas, cta):
+            assert 0 <= t0 < t1 <= tiles
+            n = np_keys if prefix else lens[b]
+            assert (tiles - 1) * keys < n <= tiles * keys
+            assert unit == (hkv * p_rt + rt if prefix else p_units + (b * Hkv + hkv) * own_rt + rt)
+            for t in range(t0, t1):
+                assert (unit, t) not in seen
+                seen[unit, t] = cta
+            assert (unit + cta) not in slots
+            slots[unit + cta] = unit
+            first, _ = ranges.get(unit, (None, None))
+            ranges[unit] = (cta if t0 == 0 else first, cta if t1 == tiles else None)
+    want = Hkv * p_rt * -(-np_keys // keys) + Hkv * own_rt * sum(-(-n // keys) for n in lens if n > 0)
+    assert len(seen) == want
+    assert all(s < p_units + B * Hkv * own_rt + n_ctas for s in slots)
+    for unit, (c0, c1) in ranges.items():  # every CTA between the two has a slot of the unit
+        assert c0 is not None and c1 is not None
+        assert all(slots[unit + c] == unit for c in range(c0, c1 + 1))
 
 
 def _simulate(units, resident, nk, nq, nbuf, nl, seed, heads=2, nwg=4):
