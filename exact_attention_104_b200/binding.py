@@ -110,7 +110,8 @@ def _ptr(x) -> int | None:
 
 def _stream_handle(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -386,17 +387,24 @@ def attention_backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causa
 
 
 # ------------------------------------------------------- bounded key/value caches
+_NO_SCOPE = contextlib.nullcontext()
+
+
 class _CacheCall:
     """Argument checks and placement of one cache call: every tensor lies on the
     device of the first, the call runs with that device current, and on
     ``stream`` (or that device's current stream), from whose memory pool the
     tensors it allocates come."""
 
+    __slots__ = ("where", "first", "device", "index", "scope")
+
     def __init__(self, where, first, stream):
         self.where = where
+        self.first = first
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             self.refuse("inputs must be CUDA tensors")
         self.device = first.device
+        self.index = first.get_device()
         # tensors of a stream given as a handle belong to that stream's pool too
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
             stream = (torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream)
@@ -405,31 +413,31 @@ class _CacheCall:
             if stream.device != self.device:
                 self.refuse("the stream belongs to another device")
             self.scope = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != self.device.index:
+        elif torch.cuda.current_device() != self.index:
             self.scope = torch.cuda.device(self.device)
         else:
-            self.scope = contextlib.nullcontext()
+            self.scope = _NO_SCOPE
 
     def refuse(self, why):
         raise FAError(FA_ERR_INVALID_ARG, f"{self.where}: {why}")
 
     def check(self, name, t, shape, dtype):
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
             self.refuse(f"{name} must be a tensor on {self.device}")
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             self.refuse(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
     def given_or_new(self, name, t, shape, dtype):
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self.first.new_empty(shape, dtype=dtype)
         self.check(name, t, shape, dtype)
         return t
 
     def scratch(self, t, need):
         """The caller's workspace, or a new one of the size needed."""
         if t is None:
-            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
-        if not isinstance(t, torch.Tensor) or t.device != self.device or not t.is_contiguous():
+            return self.first.new_empty(max(need, 256), dtype=torch.uint8)
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index or not t.is_contiguous():
             self.refuse(f"workspace must be a contiguous tensor on {self.device}")
         return t
 

@@ -347,6 +347,30 @@ fa_status cache_decode(const void* q, const void* kp, const void* vp, const void
                          ws + pl.keyw_off, di->err, s);
 }
 
+// CTAs of a cluster that selects for one (sequence, kv head): as few as can hold
+// its weights in registers, 8 at most.  16 x 8 times 8192 weights: one CTA each
+// 13 us, four 25 us; 4 x 8 times 65536 weights: eight 23 us, one 180 us.
+fa_status evict_select(const fa::EvictParams& p, cudaStream_t s) {
+  const long long units = (long long)p.B * p.Hkv;
+  int nrank = 1;
+  while (nrank < 8 && p.Ncap > fa::kEvictHeld * fa::kEvictBatch * nrank) nrank *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(units * nrank));
+  cfg.blockDim = dim3(fa::kEvictThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = nrank;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fa::fa_evict_select_kernel, p, nrank) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -464,8 +488,7 @@ fa_status fa_cache_evict(const void* k, const void* v, const float* weights, con
   p.err = di->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned units = (unsigned)(B * Hkv);
-  fa::fa_evict_select_kernel<<<units, fa::kEvictThreads, 0, s>>>(p);
-  if (launched() != FA_OK) return FA_ERR_CUDA;
+  if (evict_select(p, s) != FA_OK) return FA_ERR_CUDA;
   const dim3 grid((unsigned)((budget + fa::kEvictCopyRows - 1) / fa::kEvictCopyRows), units);
   switch (d) {
     case 64: fa::fa_evict_copy_kernel<64><<<grid, 256, 0, s>>>(p); break;

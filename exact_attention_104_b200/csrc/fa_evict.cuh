@@ -7,9 +7,15 @@
 //
 //   fa_evict_select_kernel  writes the kept indices: radix select of the
 //                           threshold (11, 11 and 10 bits of the weights as
-//                           ordered integers), then one ordered pass that
-//                           numbers what is kept
+//                           ordered integers), then one pass that numbers what
+//                           is kept
 //   fa_evict_copy_kernel    gathers K, V and the weights; bound by HBM
+//
+// The selection of a (sequence, kv head) is one cluster of CTAs: each counts its
+// share of the weights, and the counts are added up in the first CTA through
+// distributed shared memory (only bins that hold something are sent).  A share
+// of up to 8192 weights is read once and stays in registers; larger ones are
+// read four times.
 #pragma once
 
 #include "sm100.cuh"
@@ -37,112 +43,235 @@ __device__ __forceinline__ uint32_t ordered_bits(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kEvictThreads = 1024;
-
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b) {
   const int n = p.lengths ? p.lengths[b] : p.Ncap;
   return (n < 0 || n > p.Ncap) ? -1 : n;
 }
 
-__global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const EvictParams p) {
-  __shared__ int hist[2048];
-  __shared__ int warp_tot[32];
-  __shared__ int sh_bin, sh_above;
-  const int unit = blockIdx.x, b = unit / p.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = evict_len(p, b);
-  if (n < 0) {  // nothing of this sequence is written
-    if (tid == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
-    return;
-  }
-  int* index = p.index + (size_t)unit * p.out_cap;
-  const int count = min(n, p.budget);
-  for (int j = count + tid; j < p.budget; j += kEvictThreads) index[j] = -1;
-  if (unit % p.Hkv == 0 && tid == 0) p.lengths_out[b] = count;
-  if (n <= p.budget) {
-    for (int j = tid; j < n; j += kEvictThreads) index[j] = j;
-    return;
-  }
-  const int nc = n - p.recent, need = p.budget - p.recent;  // candidates, and how many of them stay
-  for (int j = tid; j < p.recent; j += kEvictThreads) index[need + j] = nc + j;
-  if (need == 0) return;
-  const float* w = p.weights + (size_t)unit * p.Ncap;
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_cluster(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
-  // threshold T: the need-th greatest of the candidates
+constexpr int kEvictThreads = 512;
+constexpr int kEvictBins = 2048;
+constexpr int kEvictBatch = 4 * kEvictThreads;  // weights of a batch: four in a row a thread
+constexpr int kEvictHeld = 4;                   // batches that a CTA can hold in registers
+
+// Inclusive sum over the CTA's threads in order; `tot` is shared scratch of one
+// int a warp.  Ends with a barrier.
+__device__ __forceinline__ int cta_scan(int x, int* tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) tot[warp] = x;
+  __syncthreads();
+  int before = lane < kEvictThreads / 32 ? tot[lane] : 0;
+#pragma unroll
+  for (int off = 1; off < kEvictThreads / 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += y;
+  }
+  before = __shfl_sync(0xffffffffu, before, max(warp - 1, 0));
+  __syncthreads();
+  return (warp ? before : 0) + x;
+}
+
+struct EvictShared {
+  int hist[kEvictBins];    // of this CTA
+  int acc[2][kEvictBins];  // of the cluster, in its first CTA; passes alternate
+  int tot[kEvictThreads / 32];
+  int result[2];  // in the first CTA: the threshold's bin, how many are above it
+  int both;
+  int kept[2];  // of this CTA: greater than the threshold, equal to it
+};
+
+// Chooses need of the weights w[0 .. nc), of which this CTA has w[j0 .. j1), and
+// writes their indices in order.  HELD: the CTA's share stays in registers.
+template <bool HELD>
+__device__ __forceinline__ void evict_select(EvictShared& sh, const float* w, int* index, int need, int j0, int j1,
+                                             int rank, int nrank) {
+  const int tid = threadIdx.x;
+  const int batches = (j1 - j0 + kEvictBatch - 1) / kEvictBatch;
+  uint32_t held[HELD ? kEvictHeld * 4 : 4];
+  auto load = [&](int bt, uint32_t* u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + bt * kEvictBatch + 4 * tid + i;
+      u[i] = j < j1 ? ordered_bits(w[j]) : 0u;
+    }
+  };
+  if (HELD)
+#pragma unroll
+    for (int bt = 0; bt < kEvictHeld; ++bt) load(bt, held + 4 * bt);
+  // calls f(batch, its four values) in order
+  auto each = [&](auto f) {
+    if (HELD) {
+#pragma unroll
+      for (int bt = 0; bt < kEvictHeld; ++bt)
+        if (bt < batches) f(bt, held + 4 * bt);
+    } else {
+#pragma unroll 1
+      for (int bt = 0; bt < batches; ++bt) {
+        load(bt, held);
+        f(bt, held);
+      }
+    }
+  };
+
+  // threshold T: the need-th greatest
+  constexpr int PER = kEvictBins / kEvictThreads;
   uint32_t prefix = 0;
-  int above = 0;  // candidates greater than every value with this prefix
+  int above = 0;          // greater than every value with this prefix
+  int gt = 0, eq = 0;     // of this thread's bins: greater than the threshold, equal to it
+  for (int e = tid; e < kEvictBins; e += kEvictThreads) sh.acc[0][e] = 0;
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
-    for (int e = tid; e < 2048; e += kEvictThreads) hist[e] = 0;
-    __syncthreads();
-    for (int j = tid; j < nc; j += kEvictThreads) {
-      const uint32_t u = ordered_bits(w[j]);
-      if (pass == 0 || (u >> (shift + bits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1 << bits) - 1)], 1);
+    for (int e = tid; e < kEvictBins; e += kEvictThreads) {
+      sh.hist[e] = 0;
+      sh.acc[(pass + 1) & 1][e] = 0;  // the next pass's
     }
-    __syncthreads();
-    // counts from the top: thread t owns bins 2047 − 2t and 2046 − 2t
-    const int c0 = hist[2047 - 2 * tid], c1 = hist[2046 - 2 * tid];
-    int x = c0 + c1;
+    if (nrank > 1) cluster_sync();
+    else __syncthreads();
+    each([&](int bt, const uint32_t* u) {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, off);
-      if (lane >= off) x += y;
+      for (int i = 0; i < 4; ++i)
+        if (j0 + bt * kEvictBatch + 4 * tid + i < j1 && (pass == 0 || (u[i] >> (shift + bits)) == prefix))
+          atomicAdd(&sh.hist[(u[i] >> shift) & ((1 << bits) - 1)], 1);
+    });
+    __syncthreads();
+    // thread t has bins 2047 − 4t .. 2044 − 4t; the CTAs add theirs up in the first
+    int mine[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[i] = sh.hist[kEvictBins - 1 - PER * tid - i];
+    if (nrank > 1) {
+      const uint32_t base = mapa_shared(smem_u32(sh.acc[pass & 1]), 0);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (mine[i]) add_cluster(base + 4 * (kEvictBins - 1 - PER * tid - i), mine[i]);
+      cluster_sync();
     }
-    if (lane == 31) warp_tot[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int t = warp_tot[lane];
+    if (rank == 0) {
+      const int* h = nrank > 1 ? sh.acc[pass & 1] : sh.hist;
+      int c[PER], x = 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, t, off);
-        if (lane >= off) t += y;
+      for (int i = 0; i < PER; ++i) x += c[i] = h[kEvictBins - 1 - PER * tid - i];
+      int before = above + cta_scan(x, sh.tot) - x;  // greater than this thread's bins
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (before < need && before + c[i] >= need) {
+          sh.result[0] = kEvictBins - 1 - PER * tid - i;
+          sh.result[1] = before;
+        }
+        before += c[i];
       }
-      warp_tot[lane] = t;
     }
-    __syncthreads();
-    const int before = above + (warp ? warp_tot[warp - 1] : 0) + x - c0 - c1;  // greater than my two bins
-    if (before < need && before + c0 >= need) {
-      sh_bin = 2047 - 2 * tid;
-      sh_above = before;
-    } else if (before + c0 < need && before + c0 + c1 >= need) {
-      sh_bin = 2046 - 2 * tid;
-      sh_above = before + c0;
+    int bin;
+    if (nrank > 1) {
+      cluster_sync();
+      const uint32_t base = mapa_shared(smem_u32(sh.result), 0);
+      bin = ld_cluster(base);
+      above = ld_cluster(base + 4);
+    } else {
+      __syncthreads();
+      bin = sh.result[0];
+      above = sh.result[1];
     }
-    __syncthreads();
-    prefix = (prefix << bits) | (uint32_t)sh_bin;
-    above = sh_above;
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = kEvictBins - 1 - PER * tid - i;
+      if (e > bin) gt += mine[i];
+      if (e == bin && pass == 2) eq = mine[i];
+    }
+    prefix = (prefix << bits) | (uint32_t)bin;
   }
   const uint32_t T = prefix;
   const int eq_need = need - above;  // of those equal to T, the first so many stay
 
-  // one pass in order: number what is kept
+  // how many of each kind lie before this CTA's share
   int gt0 = 0, eq0 = 0;
-  for (int j0 = 0; j0 < nc; j0 += kEvictThreads) {
-    const int j = j0 + tid;
-    const uint32_t u = j < nc ? ordered_bits(w[j]) : 0u;
-    const bool gt = j < nc && u > T, eq = j < nc && u == T;
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) warp_tot[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();
-    int gt_before = gt0, eq_before = eq0, gt_all = 0, eq_all = 0;
-    for (int t = 0; t < 32; ++t) {
-      const int c = warp_tot[t];
-      if (t < warp) {
-        gt_before += c & 0xffff;
-        eq_before += c >> 16;
-      }
-      gt_all += c & 0xffff;
-      eq_all += c >> 16;
+  if (nrank > 1) {
+    gt = cta_scan(gt, sh.tot);
+    eq = cta_scan(eq, sh.tot);
+    if (tid == kEvictThreads - 1) {
+      sh.kept[0] = gt;
+      sh.kept[1] = eq;
     }
-    gt_before += __popc(bg & ((1u << lane) - 1));
-    eq_before += __popc(be & ((1u << lane) - 1));
-    if (gt || (eq && eq_before < eq_need)) index[gt_before + min(eq_before, eq_need)] = j;
-    gt0 += gt_all;
-    eq0 += eq_all;
-    __syncthreads();
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+      const uint32_t base = mapa_shared(smem_u32(sh.kept), r);
+      gt0 += ld_cluster(base);
+      eq0 += ld_cluster(base + 4);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
   }
+
+  // number what is kept, in order
+  each([&](int bt, const uint32_t* u) {
+    const int j = j0 + bt * kEvictBatch + 4 * tid;
+    int g = 0, e = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      g += j + i < j1 && u[i] > T;
+      e += j + i < j1 && u[i] == T;
+    }
+    // at most kEvictBatch of each kind: both sums in one scan
+    const int both = cta_scan(g | e << 16, sh.tot);
+    int gb = gt0 + (both & 0xffff) - g, eb = eq0 + (both >> 16) - e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (j + i < j1 && u[i] > T) {
+        index[gb + min(eb, eq_need)] = j + i;
+        ++gb;
+      } else if (j + i < j1 && u[i] == T) {
+        if (eb < eq_need) index[gb + eb] = j + i;
+        ++eb;
+      }
+    }
+    if (bt + 1 < batches) {
+      if (tid == kEvictThreads - 1) sh.both = both;
+      __syncthreads();
+      gt0 += sh.both & 0xffff;
+      eq0 += sh.both >> 16;
+    }
+  });
+}
+
+// Grid: units · cluster size; cluster rank r owns the r-th share of the
+// candidates.
+__global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const EvictParams p, int nrank) {
+  __shared__ EvictShared sh;
+  const int rank = blockIdx.x % nrank, unit = blockIdx.x / nrank, b = unit / p.Hkv;
+  const int n = evict_len(p, b);
+  if (n < 0) {  // nothing of this sequence is written
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
+    return;  // the same for the whole cluster
+  }
+  int* index = p.index + (size_t)unit * p.out_cap;
+  const int count = min(n, p.budget);
+  const int all = nrank * kEvictThreads, gid = rank * kEvictThreads + threadIdx.x;
+  for (int j = count + gid; j < p.budget; j += all) index[j] = -1;
+  if (unit % p.Hkv == 0 && gid == 0) p.lengths_out[b] = count;
+  if (n <= p.budget) {
+    for (int j = gid; j < n; j += all) index[j] = j;
+    return;
+  }
+  const int nc = n - p.recent, need = p.budget - p.recent;  // candidates, and how many of them stay
+  for (int j = gid; j < p.recent; j += all) index[need + j] = nc + j;
+  if (need == 0) return;
+  const float* w = p.weights + (size_t)unit * p.Ncap;
+  const int share = (nc + nrank - 1) / nrank;
+  const int j0 = min(nc, rank * share), j1 = min(nc, j0 + share);
+  if (share <= kEvictHeld * kEvictBatch) evict_select<true>(sh, w, index, need, j0, j1, rank, nrank);
+  else evict_select<false>(sh, w, index, need, j0, j1, rank, nrank);
 }
 
 // One thread moves 16 bytes of K and of V at a time; slots count .. budget−1
