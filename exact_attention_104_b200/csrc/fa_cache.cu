@@ -228,7 +228,7 @@ template <int D>
 fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, fa::CacheList lw, fa::CacheList lt,
                        bool tc_p, bool tc_o, cudaStream_t s) {
   using W = fa::CacheCfg<D>;
-  using T = fa::FwdCfg<D, 1>;
+  using T = fa::CacheTcCfg<D>;
   lw.keys = W::KT;
   if (lw.prefix_units + lw.own_rt > 0) {
     auto kern = fa::fa_cache_split_kernel<D>;

@@ -397,25 +397,47 @@ __global__ void __launch_bounds__(256)
       return;
     }
     const CacheParts parts = cache_parts(p, lp, lo, b, h / p.G, (h % p.G) * p.Nq + i, len);
-    float M, L;
-    cache_ml(parts, lane, M, L);
+    // lane s has the m and l of part s (of 32 at a time; more than 32 parts: the
+    // running maximum and sum go on)
+    float M = -INFINITY, L = 0.f;
     constexpr int V = D / 32;  // columns of a lane
     float acc[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) acc[c] = 0.f;
     for (int s0 = 0; s0 < parts.n; s0 += 32) {
-      float f = 0.f;
-      if (s0 + lane < parts.n) {
-        const float m = parts.ml(s0 + lane).x;
-        if (m != -INFINITY) f = ex2(m - M);
-      }
       const int cnt = min(32, parts.n - s0);
-#pragma unroll 4
-      for (int t = 0; t < cnt; ++t) {
-        const float ft = __shfl_sync(0xffffffffu, f, t);
-        const float* src = parts.o(s0 + t, D) + lane * V;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < cnt) ml = parts.ml(s0 + lane);
+      const float m_new = fmaxf(M, warp_max(ml.x));
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m_new);
+      const float old = M == -INFINITY ? 0.f : ex2(M - m_new);
+      L = fmaf(L, old, warp_sum(f * ml.y));
+      M = m_new;
 #pragma unroll
-        for (int c = 0; c < V; ++c) acc[c] = fmaf(ft, src[c], acc[c]);
+      for (int c = 0; c < V; ++c) acc[c] *= old;
+      for (int t0 = 0; t0 < cnt; t0 += 8) {
+        // eight parts' loads in flight (a part that is not there: the last one, times 0)
+        float part[8][V];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float* src = parts.o(s0 + min(t0 + t, cnt - 1), D) + lane * V;
+          if constexpr (V == 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            part[t][0] = v.x, part[t][1] = v.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < V; c += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src + c);
+              part[t][c] = v.x, part[t][c + 1] = v.y, part[t][c + 2] = v.z, part[t][c + 3] = v.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float ft = t0 + t < cnt ? __shfl_sync(0xffffffffu, f, (t0 + t) & 31) : 0.f;
+#pragma unroll
+          for (int c = 0; c < V; ++c) acc[c] = fmaf(ft, part[t][c], acc[c]);
+        }
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
