@@ -196,7 +196,7 @@ CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bo
   const long long units_o = Ncap > 0 ? (long long)B * Hkv * ((R + (pl.tc_o ? 127 : 15)) / (pl.tc_o ? 128 : 16)) : 0;
   pl.units_t = (int)((pl.tc_p ? units_p : 0) + (pl.tc_o ? units_o : 0));
   pl.units_w = (int)((pl.tc_p ? 0 : units_p) + (pl.tc_o ? 0 : units_o));
-  pl.ctas_w = d == 64 ? 2 * kSms : kSms;  // as many as run at once
+  pl.ctas_w = kSms * (d == 64 ? fa::CacheCfg<64>::PER_SM : fa::CacheCfg<128>::PER_SM);  // as many as run at once
   auto take = [&](size_t bytes) {
     const size_t at = pl.bytes;
     pl.bytes += round256(bytes);
@@ -229,7 +229,7 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, f
                        bool tc_p, bool tc_o, cudaStream_t s) {
   using W = fa::CacheCfg<D>;
   using T = fa::CacheTcCfg<D>;
-  lw.keys = W::KT;
+  lw.keys = W::CH;
   if (lw.prefix_units + lw.own_rt > 0) {
     auto kern = fa::fa_cache_split_kernel<D>;
     static std::atomic<unsigned long long> allowed{0};

@@ -6,11 +6,16 @@
 //                            w[j] += Σ_r 2^(S'_rj − LSE'_r) from stored scores
 //
 // The split kernel is bound by reading K and V.  Its rows fill one m16n8k16
-// tile, so each warp works alone on runs of CH keys: TMA loads of its own ring
-// of stages, S in registers, P handed to the second product in registers, and
-// no barrier of the CTA inside the loop.  P goes into the second product as
-// the sum of two bf16 numbers (high part and remainder), so O has fp32-like
-// weights; the second product's extra instructions fit under the loads.
+// tile, so a CTA is one warp, several to an SM: TMA loads of CH keys a step
+// through a ring of stages that runs ahead into the next units, S in registers,
+// P handed to the second product in registers, and no barrier at all; what one
+// warp does between two units the others' loads cover.  (CTAs of four warps that
+// merge their results: 30 us instead of 21 for 32 x 8 caches of 64..1024 keys.)
+// K and V are read once and marked to leave L2 first, where the scores and the
+// partial results then stay: 202 -> 192 us for 8 x 32768 keys, d = 128.  P goes
+// into the second product as the sum of two bf16 numbers (high part and
+// remainder), so O has fp32-like weights; the extra instructions fit under the
+// loads.
 #pragma once
 
 #include "fa_cache_list.cuh"
@@ -43,21 +48,27 @@ constexpr float kCacheTau = 8.0f;
 
 template <int D>
 struct CacheCfg {
-  static constexpr int W = 4;                    // warps
-  static constexpr int THREADS = W * 32;
-  static constexpr int CH = D == 256 ? 16 : 32;  // keys of one warp's step
-  static constexpr int KT = W * CH;              // keys of a key tile
-  static constexpr int ST = 3;                   // stages of each warp's ring
+  static constexpr int THREADS = 32;
+  static constexpr int CH = D == 256 ? 16 : 32;  // keys of a step: the list's key tile
+  static constexpr int ST = 3;                   // stages of the ring
   static constexpr int PANEL = CH * 128;         // 64 columns x CH keys (bytes)
   static constexpr int TILE = PANEL * (D / 64);  // CH keys of K or V
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int RING = W * ST * STAGE;
-  static constexpr int BAR_OFF = RING;           // full[W][ST]
-  static constexpr int ML_OFF = BAR_OFF + W * ST * 8;  // m, l [W][16]
-  static constexpr int MISC_OFF = ML_OFF + W * 16 * 2 * 4;
-  static constexpr int SMEM_BYTES = MISC_OFF + 16 + 1024;
-  static_assert(W * 16 * D * 4 <= RING, "the warps' O fit over the ring");
-  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static constexpr int BAR_OFF = ST * STAGE;     // full[ST]
+  static constexpr int LOAD_OFF = BAR_OFF + ST * 8;
+  static constexpr int MISC_OFF = LOAD_OFF + 80;
+  static constexpr int SMEM_BYTES = MISC_OFF + 16;
+  static constexpr int PER_SM = D == 64 ? 8 : 4;  // CTAs an SM: 192 KB of stages
+  static_assert(PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory of an SM");
+};
+
+// How far the loads have come: they run up to ST steps ahead of the arithmetic,
+// into the next units too.  Kept in shared memory by lane 0.
+struct CacheLoads {
+  CacheRuns run;
+  int t;       // next key tile
+  int more;    // whether there may be another run
+  int issued;  // over all of the CTA's runs
 };
 
 template <int D>
@@ -68,235 +79,216 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
   using C = CacheCfg<D>;
   CacheRuns run;
   const int cta = blockIdx.x;
-  if (!run.start(p, list, cta)) return;  // the same for every warp
+  if (!run.start(p, list, cta)) return;
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_split[];
+  uint8_t* smem = smem_split;
   const uint32_t sbase = smem_u32(smem);
+  if (sbase & 1023) {  // dynamic shared memory starts on a 1024-byte boundary; the swizzle relies on it
+    if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevCheck);
+    return;
+  }
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::W * C::ST; ++i) mbar_init(sbase + C::BAR_OFF + 8 * i, 1);
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    for (int i = 0; i < C::ST; ++i) mbar_init(sbase + C::BAR_OFF + 8 * i, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  __syncthreads();
-  const uint32_t ring = sbase + warp * C::ST * C::STAGE;
-  const uint32_t bars = sbase + C::BAR_OFF + warp * C::ST * 8;
+  __syncwarp();
+  const uint32_t ring = sbase, bars = sbase + C::BAR_OFF;
   const WaitCtx wc{abort_flag, p.err, p.wait_cap};
-  int step0 = 0;  // steps of this warp before the run: they number the ring's stages
-  while (true) {
-  const int rows_total = run.prefix ? p.M : p.R;
-  const int len = run.len;
-  // this warp's steps: key tile t0 + i, keys warp·CH .. of it
-  int n_mine = run.t1 - run.t0;
-  if ((run.t1 - 1) * C::KT + warp * C::CH >= len) --n_mine;
-  const CUtensorMap* mk = run.prefix ? &tmKp : &tmK;
-  const CUtensorMap* mv = run.prefix ? &tmVp : &tmV;
-  const int key_base = run.prefix ? run.hkv * p.Np : (run.b * p.Hkv + run.hkv) * p.Ncap;
-  auto key_of = [&](int i) { return (run.t0 + i) * C::KT + warp * C::CH; };
-  auto issue = [&](int i) {
-    const int st = (step0 + i) % C::ST;
+  CacheLoads* ld = reinterpret_cast<CacheLoads*>(smem + C::LOAD_OFF);
+  static_assert(sizeof(CacheLoads) <= 80, "space of CacheLoads");
+  const uint64_t policy = policy_evict_first();
+  // lane 0: the next step's loads, if there is one
+  auto issue = [&] {
+    if (ld->t == ld->run.t1) {
+      if (!ld->more || !ld->run.next(p, list)) {
+        ld->more = 0;
+        return;
+      }
+      ld->t = ld->run.t0;
+    }
+    const CacheRuns& r = ld->run;
+    const int st = ld->issued % C::ST;
+    const int y = (r.prefix ? r.hkv * p.Np : (r.b * p.Hkv + r.hkv) * p.Ncap) + ld->t * C::CH;
+    const CUtensorMap* mk = r.prefix ? &tmKp : &tmK;
+    const CUtensorMap* mv = r.prefix ? &tmVp : &tmV;
     mbar_expect_tx(bars + 8 * st, C::STAGE);
 #pragma unroll
     for (int pn = 0; pn < D / 64; ++pn) {
-      tma_load_2d(ring + st * C::STAGE + pn * C::PANEL, mk, bars + 8 * st, pn * 64, key_base + key_of(i));
-      tma_load_2d(ring + st * C::STAGE + C::TILE + pn * C::PANEL, mv, bars + 8 * st, pn * 64, key_base + key_of(i));
+      tma_load_2d_hint(ring + st * C::STAGE + pn * C::PANEL, mk, bars + 8 * st, pn * 64, y, policy);
+      tma_load_2d_hint(ring + st * C::STAGE + C::TILE + pn * C::PANEL, mv, bars + 8 * st, pn * 64, y, policy);
     }
+    ++ld->t;
+    ++ld->issued;
   };
-  if (lane == 0)
-    for (int i = 0; i < C::ST && i < n_mine; ++i) issue(i);
-  if (threadIdx.x == 0) run.note(list, cta);
-
-  // this lane's two query rows: first operand fragments and last visible key
-  const int row0 = run.rt * 16 + (lane >> 2);
-  uint32_t qf[D / 16][4];
-  int last[2];
-  size_t score_row[2] = {0, 0};
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int m = row0 + 8 * x;
-    last[x] = cache_last(p, run.prefix, run.b, len, m);
-    const uint32_t* src = nullptr;
-    if (m < rows_total) {
-      src = reinterpret_cast<const uint32_t*>(p.q + cache_row(p, run.prefix, run.b, run.hkv, m) * D) + (lane & 3);
-      score_row[x] = ((size_t)(run.b * p.Hkv + run.hkv) * p.R + m) * p.cap_pad;
-    }
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      qf[ks][x] = src ? src[ks * 8] : 0u;
-      qf[ks][2 + x] = src ? src[ks * 8 + 4] : 0u;
-    }
+  if (lane == 0) {
+    ld->run = run;
+    ld->t = run.t0;
+    ld->more = 1;
+    ld->issued = 0;
+    for (int i = 0; i < C::ST; ++i) issue();
   }
+  int step = 0;  // over all of the CTA's runs: numbers the ring's stages
+  do {
+    const int rows_total = run.prefix ? p.M : p.R;
+    const int len = run.len;
+    if (lane == 0) run.note(list, cta);
 
-  float o[D / 8][4];
+    // this lane's two query rows: first operand fragments and last visible key
+    const int row0 = run.rt * 16 + (lane >> 2);
+    uint32_t qf[D / 16][4];
+    int last[2];
+    size_t score_row[2] = {0, 0};
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-  float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  bool ok = true;
-  int done = 0;
-  for (int i = 0; i < n_mine; ++i) {
-    const int st = (step0 + i) % C::ST;
-    if (!mbar_wait_warp(bars + 8 * st, ((step0 + i) / C::ST) & 1, wc, 21)) { ok = false; break; }
-    done = i + 1;
-    const int key0 = key_of(i);
-    const uint32_t kt = ring + st * C::STAGE, vt = kt + C::TILE;
-    if (key0 + C::CH > len) {
-      // what lies behind the last key may be anything, NaN too: its weight is
-      // 0, its value has to be 0 as well
-      const int first = len - key0;
-      for (int e = lane; e < (C::CH - first) * (D / 8); e += 32) {
-        const int r = first + e / (D / 8), c = e % (D / 8);
-        *reinterpret_cast<uint4*>(smem + (vt - sbase) + (c >> 3) * C::PANEL + r * 128 + (c & 7) * 16) =
-            make_uint4(0, 0, 0, 0);
+    for (int x = 0; x < 2; ++x) {
+      const int m = row0 + 8 * x;
+      last[x] = cache_last(p, run.prefix, run.b, len, m);
+      const uint32_t* src = nullptr;
+      if (m < rows_total) {
+        src = reinterpret_cast<const uint32_t*>(p.q + cache_row(p, run.prefix, run.b, run.hkv, m) * D) + (lane & 3);
+        score_row[x] = ((size_t)(run.b * p.Hkv + run.hkv) * p.R + m) * p.cap_pad;
       }
-      __syncwarp();
-    }
-    // S = Q Kᵀ
-    float s[C::CH / 8][4];
-#pragma unroll
-    for (int nt = 0; nt < C::CH / 8; nt += 2) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = s[nt + 1][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        const int key = (nt + (lane >> 4)) * 8 + (lane & 7);
-        const int c = 2 * ks + ((lane >> 3) & 1);
-        uint32_t kb[4];
-        ldsm_x4(kb, kt + (c >> 3) * C::PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-        mma16816(s[nt], qf[ks], kb[0], kb[1]);
-        mma16816(s[nt + 1], qf[ks], kb[2], kb[3]);
+        qf[ks][x] = src ? src[ks * 8] : 0u;
+        qf[ks][2 + x] = src ? src[ks * 8 + 4] : 0u;
       }
     }
-    // to log2 units, masked; running maximum
-    float mx[2] = {-INFINITY, -INFINITY};
+
+    float o[D / 8][4];
 #pragma unroll
-    for (int nt = 0; nt < C::CH / 8; ++nt)
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + nt * 8 + 2 * (lane & 3) + (e & 1);
-        s[nt][e] = key > last[e >> 1] ? -INFINITY : s[nt][e] * p.scale_log2;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool ok = true;
+    for (int t = run.t0; t < run.t1; ++t, ++step) {
+      const int st = step % C::ST;
+      if (!mbar_wait_warp(bars + 8 * st, (step / C::ST) & 1, wc, 21)) { ok = false; break; }
+      const int key0 = t * C::CH;
+      const uint32_t kt = ring + st * C::STAGE, vt = kt + C::TILE;
+      if (key0 + C::CH > len) {
+        // what lies behind the last key may be anything, NaN too: its weight is
+        // 0, its value has to be 0 as well
+        const int first = len - key0;
+        for (int e = lane; e < (C::CH - first) * (D / 8); e += 32) {
+          const int r = first + e / (D / 8), c = e % (D / 8);
+          *reinterpret_cast<uint4*>(smem + (vt - sbase) + (c >> 3) * C::PANEL + r * 128 + (c & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before later loads into the stage
+        __syncwarp();
       }
-    if (p.scores && !run.prefix) {
+      // S = Q Kᵀ
+      float s[C::CH / 8][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (row0 + 8 * x < rows_total)
+      for (int nt = 0; nt < C::CH / 8; nt += 2) {
 #pragma unroll
-          for (int nt = 0; nt < C::CH / 8; ++nt)
-            *reinterpret_cast<float2*>(p.scores + score_row[x] + key0 + nt * 8 + 2 * (lane & 3)) =
-                make_float2(s[nt][2 * x], s[nt][2 * x + 1]);
+        for (int e = 0; e < 4; ++e) s[nt][e] = s[nt + 1][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int key = (nt + (lane >> 4)) * 8 + (lane & 7);
+          const int c = 2 * ks + ((lane >> 3) & 1);
+          uint32_t kb[4];
+          ldsm_x4(kb, kt + (c >> 3) * C::PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+          mma16816(s[nt], qf[ks], kb[0], kb[1]);
+          mma16816(s[nt + 1], qf[ks], kb[2], kb[3]);
+        }
+      }
+      // to log2 units, masked; running maximum
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int nt = 0; nt < C::CH / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = key0 + nt * 8 + 2 * (lane & 3) + (e & 1);
+          s[nt][e] = key > last[e >> 1] ? -INFINITY : s[nt][e] * p.scale_log2;
+          mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
+        }
+      if (p.scores && !run.prefix) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (row0 + 8 * x < rows_total)
+#pragma unroll
+            for (int nt = 0; nt < C::CH / 8; ++nt)
+              *reinterpret_cast<float2*>(p.scores + score_row[x] + key0 + nt * 8 + 2 * (lane & 3)) =
+                  make_float2(s[nt][2 * x], s[nt][2 * x + 1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+      }
+      // the reference maximum moves only when a row's maximum passes it by more
+      // than kCacheTau: l and O share it, so the result is the same
+      if (__any_sync(0xffffffffu, mx[0] > m_ref[0] + kCacheTau || mx[1] > m_ref[1] + kCacheTau)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float m_new = fmaxf(m_ref[x], mx[x]);
+          const float a = m_new == -INFINITY ? 1.f : ex2(m_ref[x] - m_new);
+          m_ref[x] = m_new;
+          l[x] *= a;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[n][2 * x] *= a;
+            o[n][2 * x + 1] *= a;
+          }
+        }
+      }
+      const float sub[2] = {m_ref[0] == -INFINITY ? 0.f : m_ref[0], m_ref[1] == -INFINITY ? 0.f : m_ref[1]};
+#pragma unroll
+      for (int nt = 0; nt < C::CH / 8; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[nt][e] = ex2(s[nt][e] - sub[e >> 1]);
+          l[e >> 1] += s[nt][e];
+        }
+      // O += P V, P as high part plus remainder
+#pragma unroll
+      for (int kk = 0; kk < C::CH / 16; ++kk) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float a = s[2 * kk + (f >> 1)][2 * (f & 1)], c = s[2 * kk + (f >> 1)][2 * (f & 1) + 1];
+          hi[f] = pack_bf16(a, c);
+          lo[f] = pack_bf16(a - bf_lo(hi[f]), c - bf_hi(hi[f]));
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 2) {
+          const int key = kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+          const int c = n + (lane >> 4);
+          uint32_t vb[4];
+          ldsm_x4_t(vb, vt + (c >> 3) * C::PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+          mma16816(o[n], hi, vb[0], vb[1]);
+          mma16816(o[n + 1], hi, vb[2], vb[3]);
+          mma16816(o[n], lo, vb[0], vb[1]);
+          mma16816(o[n + 1], lo, vb[2], vb[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) issue();
+    }
+    if (!ok) {  // no exit before the copies in flight have landed
+      if (lane == 0)
+        for (int i = step; i < ld->issued; ++i) mbar_wait_inflight(bars + 8 * (i % C::ST), (i / C::ST) & 1, wc, 22);
+      return;
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      if (row0 + 8 * x >= rows_total) continue;
+      const size_t slot = (size_t)(run.unit + cta) * 16 + (lane >> 2) + 8 * x;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(list.part_o + slot * D + n * 8 + 2 * (lane & 3)) =
+            make_float2(o[n][2 * x], o[n][2 * x + 1]);
+      if ((lane & 3) == 0) *reinterpret_cast<float2*>(list.part_ml + slot * 2) = make_float2(m_ref[x], l[x]);
     }
-    // the reference maximum moves only when a row's maximum passes it by more
-    // than kCacheTau: l and O share it, so the result is the same
-    if (__any_sync(0xffffffffu, mx[0] > m_ref[0] + kCacheTau || mx[1] > m_ref[1] + kCacheTau)) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float m_new = fmaxf(m_ref[x], mx[x]);
-        const float a = m_new == -INFINITY ? 1.f : ex2(m_ref[x] - m_new);
-        m_ref[x] = m_new;
-        l[x] *= a;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][2 * x] *= a;
-          o[n][2 * x + 1] *= a;
-        }
-      }
-    }
-    const float sub[2] = {m_ref[0] == -INFINITY ? 0.f : m_ref[0], m_ref[1] == -INFINITY ? 0.f : m_ref[1]};
-#pragma unroll
-    for (int nt = 0; nt < C::CH / 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[nt][e] = ex2(s[nt][e] - sub[e >> 1]);
-        l[e >> 1] += s[nt][e];
-      }
-    // O += P V, P as high part plus remainder
-#pragma unroll
-    for (int kk = 0; kk < C::CH / 16; ++kk) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const float a = s[2 * kk + (f >> 1)][2 * (f & 1)], c = s[2 * kk + (f >> 1)][2 * (f & 1) + 1];
-        hi[f] = pack_bf16(a, c);
-        lo[f] = pack_bf16(a - bf_lo(hi[f]), c - bf_hi(hi[f]));
-      }
-#pragma unroll
-      for (int n = 0; n < D / 8; n += 2) {
-        const int key = kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
-        const int c = n + (lane >> 4);
-        uint32_t vb[4];
-        ldsm_x4_t(vb, vt + (c >> 3) * C::PANEL + key * 128 + (((c & 7) ^ (key & 7)) << 4));
-        mma16816(o[n], hi, vb[0], vb[1]);
-        mma16816(o[n + 1], hi, vb[2], vb[3]);
-        mma16816(o[n], lo, vb[0], vb[1]);
-        mma16816(o[n + 1], lo, vb[2], vb[3]);
-      }
-    }
-    __syncwarp();
-    if (lane == 0 && i + C::ST < n_mine) issue(i + C::ST);
-  }
-  // a warp that gave up waits for its own copies in flight
-  if (!ok && lane == 0)
-    for (int i = done; i < n_mine && i < done + C::ST; ++i)
-      mbar_wait_inflight(bars + 8 * ((step0 + i) % C::ST), ((step0 + i) / C::ST) & 1, wc, 22);
-  step0 += n_mine;
-
-  // merge the warps: m, l and O of every row through shared memory
-  float* ml = reinterpret_cast<float*>(smem + C::ML_OFF);
-  float* red = reinterpret_cast<float*>(smem);  // [W][16][D], over the ring
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-    if ((lane & 3) == 0) {
-      ml[(warp * 16 + (lane >> 2) + 8 * x) * 2] = m_ref[x];
-      ml[(warp * 16 + (lane >> 2) + 8 * x) * 2 + 1] = l[x];
-    }
-  }
-  __syncthreads();  // every warp has read its last stage
-#pragma unroll
-  for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-      *reinterpret_cast<float2*>(red + ((size_t)warp * 16 + (lane >> 2) + 8 * x) * D + n * 8 + 2 * (lane & 3)) =
-          make_float2(o[n][2 * x], o[n][2 * x + 1]);
-  __syncthreads();
-  if (*abort_flag) return;  // set before the last barrier or never: the same for all
-  const int rows = min(16, rows_total - run.rt * 16);
-  const size_t slot0 = (size_t)(run.unit + cta) * 16;
-  for (int e = threadIdx.x; e < rows * (D / 4); e += C::THREADS) {
-    const int r = e / (D / 4), c = e - r * (D / 4);
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < C::W; ++w) M = fmaxf(M, ml[(w * 16 + r) * 2]);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-#pragma unroll
-    for (int w = 0; w < C::W; ++w) {
-      const float mw = ml[(w * 16 + r) * 2];
-      const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-      const float4 v = reinterpret_cast<const float4*>(red + ((size_t)w * 16 + r) * D)[c];
-      L = fmaf(f, ml[(w * 16 + r) * 2 + 1], L);
-      sum.x = fmaf(f, v.x, sum.x);
-      sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z);
-      sum.w = fmaf(f, v.w, sum.w);
-    }
-    reinterpret_cast<float4*>(list.part_o + (slot0 + r) * D)[c] = sum;
-    if (c == 0) *reinterpret_cast<float2*>(list.part_ml + (slot0 + r) * 2) = make_float2(M, L);
-  }
-  if (!run.next(p, list)) return;
-  fence_proxy_async_smem();  // the next run's loads overwrite what was written here
-  __syncthreads();
-  }
+  } while (run.next(p, list));
 }
 
 // Where the partial results of one query row lie, and how many there are: a
@@ -373,7 +365,7 @@ __device__ __forceinline__ void cache_ml(const CacheParts& parts, int lane, floa
 }
 
 // Keys of a CTA of the weights' part of the finish kernel.
-constexpr int kCacheWeightKeys = 1024;
+constexpr int kCacheWeightKeys = 2048;
 
 // CTAs 0 .. n_combine−1: O and LSE, one query row a warp; a row that no key is
 // visible to has O = 0 and LSE = −inf.  The CTAs behind them (only with stored
@@ -451,7 +443,7 @@ __global__ void __launch_bounds__(256)
   __shared__ float lse2[16];
   const int per = (p.Ncap + kCacheWeightKeys - 1) / kCacheWeightKeys;
   const int unit = (blockIdx.x - n_combine) / per, b = unit / p.Hkv;
-  const int j = (blockIdx.x - n_combine) % per * kCacheWeightKeys + 4 * (int)threadIdx.x;
+  const int j0 = (blockIdx.x - n_combine) % per * kCacheWeightKeys + 4 * (int)threadIdx.x;
   const int len = cache_len(p, b);
   if (len < 0) {  // this sequence's weights stay as they are
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
@@ -464,24 +456,29 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) lse2[r] = L > 0.f ? M + lg2(L) : INFINITY;
   }
   __syncthreads();
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  if (j < len) {  // scores are stored up to a multiple of 32 keys
-    const float* src = p.scores + (size_t)unit * p.R * p.cap_pad + j;
-#pragma unroll 4
-    for (int r = 0; r < p.R; ++r) {
-      const float4 s = *reinterpret_cast<const float4*>(src + (size_t)r * p.cap_pad);
-      acc[0] += ex2(s.x - lse2[r]);
-      acc[1] += ex2(s.y - lse2[r]);
-      acc[2] += ex2(s.z - lse2[r]);
-      acc[3] += ex2(s.w - lse2[r]);
-    }
-  }
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    if (j + t >= p.Ncap) continue;
-    const size_t at = (size_t)unit * p.Ncap + j + t;
-    const float w = p.weights ? p.weights[at] : 0.f;
-    p.weights_out[at] = j + t < len ? w + acc[t] : w;
+  for (int c = 0; c < kCacheWeightKeys / 1024; ++c) {
+    const int j = j0 + c * 1024;
+    if (j >= p.Ncap) break;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (j < len) {  // scores are stored up to a multiple of 16 keys at least
+      const float* src = p.scores + (size_t)unit * p.R * p.cap_pad + j;
+#pragma unroll 8
+      for (int r = 0; r < p.R; ++r) {
+        const float4 s = *reinterpret_cast<const float4*>(src + (size_t)r * p.cap_pad);
+        acc[0] += ex2(s.x - lse2[r]);
+        acc[1] += ex2(s.y - lse2[r]);
+        acc[2] += ex2(s.z - lse2[r]);
+        acc[3] += ex2(s.w - lse2[r]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (j + t >= p.Ncap) continue;
+      const size_t at = (size_t)unit * p.Ncap + j + t;
+      const float w = p.weights ? p.weights[at] : 0.f;
+      p.weights_out[at] = j + t < len ? w + acc[t] : w;
+    }
   }
 }
 

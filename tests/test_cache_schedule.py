@@ -133,7 +133,7 @@ def _cache_runs(p_units, p_rt, np_keys, Hkv, own_rt, lens, keys, n_ctas, cta):
 @pytest.mark.parametrize("seed", range(60))
 def test_cache_work_list(seed):
     rng = random.Random(seed)
-    keys, n_ctas = rng.choice([(128, 148), (64, 148), (128, 296)])
+    keys, n_ctas = rng.choice([(128, 148), (16, 592), (32, 1184)])
     B, Hkv, own_rt = rng.randint(1, 40), rng.randint(1, 4), rng.choice([0, 1, 1, 2])
     p_rt = rng.choice([0, 1, 3]) if own_rt else 1
     np_keys = rng.choice([rng.randint(1, 300), rng.randint(1, 30000)])
