@@ -43,6 +43,25 @@ fa_status allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done
 
 fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
+// Launch with leave to start before the kernel in front has finished (see
+// grid_wait).
+template <class... P, class... A>
+fa_status launch_early(void (*kern)(P...), unsigned grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...) == cudaSuccess) return FA_OK;
+  cudaGetLastError();
+  return FA_ERR_CUDA;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // No output may overlap an input or another output.
@@ -230,19 +249,45 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, f
   using W = fa::CacheCfg<D>;
   using T = fa::CacheTcCfg<D>;
   lw.keys = W::CH;
-  if (lw.prefix_units + lw.own_rt > 0) {
-    auto kern = fa::fa_cache_split_kernel<D>;
-    static std::atomic<unsigned long long> allowed{0};
-    if (allow_smem(kern, W::SMEM_BYTES, allowed) != FA_OK) return FA_ERR_CUDA;
-    kern<<<(unsigned)lw.n_ctas, W::THREADS, W::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p, lw);
-    if (launched() != FA_OK) return FA_ERR_CUDA;
+  const bool have_w = lw.prefix_units + lw.own_rt > 0, have_t = lt.prefix_units + lt.own_rt > 0;
+  auto tiles = [](const fa::CacheList& l, long long n) { return (n + l.keys - 1) / l.keys; };
+  for (const fa::CacheList& l : {lw, lt})
+    if (l.prefix_units * tiles(l, p.Np) + (long long)p.B * p.Hkv * l.own_rt * tiles(l, p.Ncap) >= (1LL << 31) - (1 << 20))
+      return FA_ERR_UNSUPPORTED;
+  if (have_w && have_t) {
+    // The prefix's many rows and the few rows of each sequence: both kernels at
+    // once, on SMs of their own, since one is bound by its softmax and the other
+    // by reading keys.  The tcgen05 kernel goes first and fills its SMs' shared
+    // memory; the split kernel, launched before that one ends, gets the others.
+    // Shares by the SM time that each was measured to take (us): a key tile there,
+    // a step here; how full the caches are only the device knows: two thirds.
+    // One after the other, each on all SMs: 32 sequences behind 8192 keys (d 128)
+    // 41 us instead of BATCH, 24 x 5 rows behind 20001 keys (d 256) 125 instead of DRAFT.
+    const double tile_us = D == 64 ? 1.3 : (D == 128 ? 1.8 : 3.2), step_us = D == 64 ? 0.28 : (D == 128 ? 0.56 : 0.39);
+    const double cost_t = tile_us * lt.prefix_units * tiles(lt, p.Np);
+    const double cost_w = step_us * p.B * p.Hkv * tiles(lw, p.Ncap) * 2 / 3;
+    lt.n_ctas = std::min(kSms - 8, std::max(8, (int)(kSms * cost_t / (cost_t + cost_w) + 0.5)));
+    lw.n_ctas = (kSms - lt.n_ctas) * W::PER_SM;
   }
-  if (lt.prefix_units + lt.own_rt > 0) {
+  if (have_t) {
     auto kern = fa::fa_cache_tc_kernel<D>;
     static std::atomic<unsigned long long> allowed{0};
     if (allow_smem(kern, T::SMEM_BYTES, allowed) != FA_OK) return FA_ERR_CUDA;
     kern<<<(unsigned)lt.n_ctas, T::THREADS, T::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p, lt);
     if (launched() != FA_OK) return FA_ERR_CUDA;
+  }
+  if (have_w) {
+    auto kern = fa::fa_cache_split_kernel<D>;
+    static std::atomic<unsigned long long> allowed{0};
+    if (allow_smem(kern, W::SMEM_BYTES, allowed) != FA_OK) return FA_ERR_CUDA;
+    if (have_t) {
+      if (launch_early(kern, (unsigned)lw.n_ctas, W::THREADS, W::SMEM_BYTES, s, maps[0], maps[1], maps[2], maps[3], p,
+                       lw) != FA_OK)
+        return FA_ERR_CUDA;
+    } else {
+      kern<<<(unsigned)lw.n_ctas, W::THREADS, W::SMEM_BYTES, s>>>(maps[0], maps[1], maps[2], maps[3], p, lw);
+      if (launched() != FA_OK) return FA_ERR_CUDA;
+    }
   }
   const unsigned combine = (unsigned)(((long long)p.B * p.Hq * p.Nq + 7) / 8);
   const unsigned per = p.weights_out ? (unsigned)((p.Ncap + fa::kCacheWeightKeys - 1) / fa::kCacheWeightKeys) : 0;

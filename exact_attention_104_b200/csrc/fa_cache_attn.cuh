@@ -79,13 +79,19 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
   using C = CacheCfg<D>;
   CacheRuns run;
   const int cta = blockIdx.x;
-  if (!run.start(p, list, cta)) return;
+  // beside the tcgen05 kernel: what comes after this kernel reads the results of
+  // both, so no CTA leaves before that one has finished
+  if (!run.start(p, list, cta)) {
+    grid_wait();
+    return;
+  }
 
   extern __shared__ __align__(1024) uint8_t smem_split[];
   uint8_t* smem = smem_split;
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023) {  // dynamic shared memory starts on a 1024-byte boundary; the swizzle relies on it
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevCheck);
+    grid_wait();
     return;
   }
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF);
@@ -274,6 +280,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
     if (!ok) {  // no exit before the copies in flight have landed
       if (lane == 0)
         for (int i = step; i < ld->issued; ++i) mbar_wait_inflight(bars + 8 * (i % C::ST), (i / C::ST) & 1, wc, 22);
+      grid_wait();
       return;
     }
 #pragma unroll
@@ -289,6 +296,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS)
       if ((lane & 3) == 0) *reinterpret_cast<float2*>(list.part_ml + slot * 2) = make_float2(m_ref[x], l[x]);
     }
   } while (run.next(p, list));
+  grid_wait();
 }
 
 // Where the partial results of one query row lie, and how many there are: a

@@ -80,12 +80,11 @@ struct CacheRuns {
   bool prefix;
   int t0, t1;  // key tiles of the run
   int tiles;   // of the unit
-  long long left;
+  int left;    // key tiles of this CTA from t0 on
 
   __device__ __forceinline__ int tiles_of(const CacheList& l, int n) const { return n > 0 ? (n + l.keys - 1) / l.keys : 0; }
-  __device__ __forceinline__ long long own_tiles(const CacheParams& p, const CacheList& l, int bb) const {
-    if (bb >= p.B || l.own_rt == 0) return 0;
-    return (long long)p.Hkv * l.own_rt * tiles_of(l, cache_len(p, bb));
+  __device__ __forceinline__ int own_tiles(const CacheParams& p, const CacheList& l, int bb) const {
+    return bb < p.B ? p.Hkv * l.own_rt * tiles_of(l, cache_len(p, bb)) : 0;
   }
   __device__ __forceinline__ void set_prefix(const CacheParams& p, const CacheList& l) {
     prefix = true;
@@ -98,38 +97,49 @@ struct CacheRuns {
   __device__ __forceinline__ void set_unit(const CacheParams& p, const CacheList& l) {
     unit = l.prefix_units + (b * p.Hkv + hkv) * l.own_rt + rt;
   }
-  __device__ __forceinline__ void set_end() { t1 = (int)min((long long)tiles, t0 + left); }
+  __device__ __forceinline__ void set_end() { t1 = min(tiles, t0 + left); }
 
-  // False if this CTA has nothing to do.  The whole warp calls it.
+  // False if this CTA has nothing to do.  The whole warp calls it.  (The host
+  // refuses lists of 2^31 - 2^20 key tiles and more.)
   __device__ __forceinline__ bool start(const CacheParams& p, const CacheList& l, int cta) {
     const int lane = threadIdx.x & 31;
-    const long long in_prefix = (long long)l.prefix_units * tiles_of(l, p.Np);
-    long long all = 0;
-    for (int b0 = 0; b0 < p.B && l.own_rt > 0; b0 += 32) all += own_tiles(p, l, b0 + lane);
+    const int in_prefix = l.prefix_units > 0 ? l.prefix_units * tiles_of(l, p.Np) : 0;
+    // 32 sequences at a time: their tiles and the sum up to each; the first 32
+    // (mostly all) are needed twice and stay
+    auto scan = [&](int b0, int& mine) {
+      mine = own_tiles(p, l, b0 + lane);
+      int sum = mine;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    all += in_prefix;
-    const long long per = (all + l.n_ctas - 1) / l.n_ctas;
-    long long x = per * cta;
-    if (x >= all) return false;
-    left = min(all, x + per) - x;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      return sum;
+    };
+    int mine = 0, sum = 0, all = in_prefix;
+    if (l.own_rt > 0) {
+      sum = scan(0, mine);
+      all += __shfl_sync(0xffffffffu, sum, 31);
+      for (int b0 = 32; b0 < p.B; b0 += 32) {
+        int m;
+        all += __shfl_sync(0xffffffffu, scan(b0, m), 31);
+      }
+    }
+    const unsigned per = ((unsigned)all + l.n_ctas - 1) / (unsigned)l.n_ctas;
+    if ((unsigned long long)per * cta >= (unsigned)all) return false;
+    int x = (int)(per * cta);
+    left = min(all - x, (int)per);
     if (x < in_prefix) {
-      unit = (int)(x / tiles_of(l, p.Np));
+      unit = (unsigned)x / (unsigned)tiles_of(l, p.Np);
       set_prefix(p, l);
-      t0 = (int)(x - (long long)unit * tiles);
+      t0 = x - unit * tiles;
       set_end();
       return true;
     }
     x -= in_prefix;
     prefix = false;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const long long mine = own_tiles(p, l, b0 + lane);
-      long long sum = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-      }
+      if (b0 > 0) sum = scan(b0, mine);
       const uint32_t past = __ballot_sync(0xffffffffu, sum > x);
       if (past) {
         const int ln = __ffs(past) - 1;
@@ -141,10 +151,10 @@ struct CacheRuns {
     }
     len = cache_len(p, b);
     tiles = tiles_of(l, len);
-    const int u = (int)(x / tiles);  // within the sequence
-    hkv = u / l.own_rt;
+    const int u = (unsigned)x / (unsigned)tiles;  // within the sequence
+    hkv = (unsigned)u / (unsigned)l.own_rt;
     rt = u - hkv * l.own_rt;
-    t0 = (int)(x - (long long)u * tiles);
+    t0 = x - u * tiles;
     set_unit(p, l);
     set_end();
     return true;

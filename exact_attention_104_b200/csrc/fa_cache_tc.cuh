@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(CacheTcCfg<D>::THREADS, 1)
                        const CacheParams p, const CacheList list) {
   using C = CacheTcCfg<D>;
   using Ord = KVOrder;
+  grid_trigger();  // the split kernel beside this one, see launch_cache
   CacheRuns run;
   const int cta = blockIdx.x;
   if (!run.start(p, list, cta)) return;  // the same for every warp
@@ -376,10 +377,12 @@ __global__ void __launch_bounds__(CacheTcCfg<D>::THREADS, 1)
           }
           __syncwarp();
           const int mine = min(32, rows - run.rt * C::BM - quarter * 32);  // rows of this warp (may be <= 0)
-          for (int e = lane; e < mine * NC; e += 32) {
-            const int r = e / NC, c = e % NC;
-            *reinterpret_cast<float4*>(list.part_o + (slot + r) * D + col0 + 4 * c) =
-                stage[r * NC + (c ^ (r & (NC - 1)))];
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const int r = (i * 32 + lane) / NC, c = lane % NC;
+            if (r < mine)
+              *reinterpret_cast<float4*>(list.part_o + (slot + r) * D + col0 + 4 * c) =
+                  stage[r * NC + (c ^ (r & (NC - 1)))];
           }
           __syncwarp();
         }
