@@ -7,7 +7,6 @@ library is missing or the device is unsupported, calls raise ``FAError``.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -387,65 +386,62 @@ def attention_backward_varlen(q, k, v, o, lse, do, cu_seqlens, max_seqlen, causa
 
 
 # ------------------------------------------------------- bounded key/value caches
-_NO_SCOPE = contextlib.nullcontext()
-
-
 class _CacheCall:
-    """Argument checks and placement of one cache call: every tensor lies on the
-    device of the first, the call runs with that device current, and on
-    ``stream`` (or that device's current stream), from whose memory pool the
-    tensors it allocates come."""
+    """Where one cache call runs: every tensor lies on the device of the first,
+    the call runs with that device current, and on ``stream`` (or that device's
+    current stream), from whose memory pool the tensors it allocates come.
+    ``scope`` is None where that is the state already."""
 
-    __slots__ = ("where", "first", "device", "index", "scope")
+    __slots__ = ("where", "device", "index", "scope")
 
     def __init__(self, where, first, stream):
         self.where = where
-        self.first = first
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             self.refuse("inputs must be CUDA tensors")
         self.device = first.device
         self.index = first.get_device()
-        # tensors of a stream given as a handle belong to that stream's pool too
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = (torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream)
-                      else torch.cuda.default_stream(self.device))
+        self.scope = None
         if stream is not None:
+            # tensors of a stream given as a handle belong to that stream's pool too
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(int(stream), device=self.device) if int(stream)
+                          else torch.cuda.default_stream(self.device))
             if stream.device != self.device:
                 self.refuse("the stream belongs to another device")
             self.scope = torch.cuda.stream(stream)
         elif torch.cuda.current_device() != self.index:
             self.scope = torch.cuda.device(self.device)
-        else:
-            self.scope = _NO_SCOPE
 
     def refuse(self, why):
         raise FAError(FA_ERR_INVALID_ARG, f"{self.where}: {why}")
 
     def check(self, name, t, shape, dtype):
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+                and t.is_contiguous()):
+            return
         if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
             self.refuse(f"{name} must be a tensor on {self.device}")
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-            self.refuse(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+        self.refuse(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)} "
+                    f"with strides {list(t.stride())}")
 
-    def given_or_new(self, name, t, shape, dtype):
-        if t is None:
-            return self.first.new_empty(shape, dtype=dtype)
-        self.check(name, t, shape, dtype)
-        return t
-
-    def scratch(self, t, need):
+    def scratch(self, t, first, need):
         """The caller's workspace, or a new one of the size needed."""
         if t is None:
-            return self.first.new_empty(max(need, 256), dtype=torch.uint8)
+            return first.new_empty(max(need, 256), dtype=torch.uint8)
         if not isinstance(t, torch.Tensor) or t.get_device() != self.index or not t.is_contiguous():
             self.refuse(f"workspace must be a contiguous tensor on {self.device}")
         return t
 
+    def dims(self, q, k):
+        if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+            self.refuse("q and k must be [B, H, N, d]")
+        return (*q.shape, k.shape[1], k.shape[2])
 
-def _cache_dims(call, q, k):
-    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
-        call.refuse("q and k must be [B, H, N, d]")
-    return (*q.shape, k.shape[1], k.shape[2])
+    def run(self, body):
+        if self.scope is None:
+            return body()
+        with self.scope:
+            return body()
 
 
 def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lengths=None, causal=False, scale=None, out=None, lse=None,
@@ -456,26 +452,35 @@ def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lengths=None, causal=Fa
     its last Nq positions (see fa_fwd_decode_prefix).  Np and Ncap may be 0.
     Returns (o bf16 [B,Hq,Nq,d], lse fp32 [B,Hq,Nq])."""
     call = _CacheCall("attention_decode_prefix", q, stream)
-    B, Hq, Nq, d, Hkv, Ncap = _cache_dims(call, q, k)
+    B, Hq, Nq, d, Hkv, Ncap = call.dims(q, k)
     if not isinstance(k_prefix, torch.Tensor) or k_prefix.dim() != 3:
         call.refuse("k_prefix must be [Hkv, Np, d]")
     Np = k_prefix.shape[1]
-    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
-    for name, t in (("k", k), ("v", v)):
-        call.check(name, t, (B, Hkv, Ncap, d), torch.bfloat16)
-    for name, t in (("k_prefix", k_prefix), ("v_prefix", v_prefix)):
-        call.check(name, t, (Hkv, Np, d), torch.bfloat16)
+    check, own, pre = call.check, (B, Hkv, Ncap, d), (Hkv, Np, d)
+    check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    check("k", k, own, torch.bfloat16)
+    check("v", v, own, torch.bfloat16)
+    check("k_prefix", k_prefix, pre, torch.bfloat16)
+    check("v_prefix", v_prefix, pre, torch.bfloat16)
     if lengths is not None:
-        call.check("lengths", lengths, (B,), torch.int32)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with call.scope:
-        out = call.given_or_new("out", out, (B, Hq, Nq, d), torch.bfloat16)
-        lse = call.given_or_new("lse", lse, (B, Hq, Nq), torch.float32)
-        workspace = call.scratch(workspace, fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d))
-        _check(fa_fwd_decode_prefix(q, k_prefix, v_prefix, k, v, lengths, out, lse, B, Hq, Hkv, Nq, Np, Ncap, d,
-                                    causal, scale, workspace, workspace.numel() * workspace.element_size()),
-               "fa_fwd_decode_prefix")
-    return out, lse
+        check("lengths", lengths, (B,), torch.int32)
+
+    def body():
+        o = torch.empty_like(q) if out is None else out
+        ls = q.new_empty((B, Hq, Nq), dtype=torch.float32) if lse is None else lse
+        if out is not None:
+            check("out", out, (B, Hq, Nq, d), torch.bfloat16)
+        if lse is not None:
+            check("lse", lse, (B, Hq, Nq), torch.float32)
+        ws = call.scratch(workspace, q, lib().fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d))
+        _check(lib().fa_fwd_decode_prefix(
+            q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(),
+            None if lengths is None else lengths.data_ptr(), o.data_ptr(), ls.data_ptr(), B, Hq, Hkv, Nq, Np, Ncap, d,
+            1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
+            _stream_handle(None)), "fa_fwd_decode_prefix")
+        return o, ls
+
+    return call.run(body)
 
 
 def attention_decode_weights(q, k, v, weights=None, lengths=None, causal=False, scale=None, out=None, lse=None,
@@ -486,24 +491,35 @@ def attention_decode_weights(q, k, v, weights=None, lengths=None, causal=False, 
     tensor as weights and weights_out updates it in place (see
     fa_fwd_decode_weights).  Returns (o, lse, weights_out)."""
     call = _CacheCall("attention_decode_weights", q, stream)
-    B, Hq, Nq, d, Hkv, Nk = _cache_dims(call, q, k)
-    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
-    for name, t in (("k", k), ("v", v)):
-        call.check(name, t, (B, Hkv, Nk, d), torch.bfloat16)
+    B, Hq, Nq, d, Hkv, Nk = call.dims(q, k)
+    check, own = call.check, (B, Hkv, Nk, d)
+    check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    check("k", k, own, torch.bfloat16)
+    check("v", v, own, torch.bfloat16)
     if weights is not None:
-        call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+        check("weights", weights, (B, Hkv, Nk), torch.float32)
     if lengths is not None:
-        call.check("lengths", lengths, (B,), torch.int32)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with call.scope:
-        out = call.given_or_new("out", out, (B, Hq, Nq, d), torch.bfloat16)
-        lse = call.given_or_new("lse", lse, (B, Hq, Nq), torch.float32)
-        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
-        workspace = call.scratch(workspace, fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
-        _check(fa_fwd_decode_weights(q, k, v, lengths, weights, weights_out, out, lse, B, Hq, Hkv, Nq, Nk, d, causal,
-                                     scale, workspace, workspace.numel() * workspace.element_size()),
-               "fa_fwd_decode_weights")
-    return out, lse, weights_out
+        check("lengths", lengths, (B,), torch.int32)
+
+    def body():
+        o = torch.empty_like(q) if out is None else out
+        ls = q.new_empty((B, Hq, Nq), dtype=torch.float32) if lse is None else lse
+        wo = q.new_empty((B, Hkv, Nk), dtype=torch.float32) if weights_out is None else weights_out
+        if out is not None:
+            check("out", out, (B, Hq, Nq, d), torch.bfloat16)
+        if lse is not None:
+            check("lse", lse, (B, Hq, Nq), torch.float32)
+        if weights_out is not None:
+            check("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
+        ws = call.scratch(workspace, q, lib().fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        _check(lib().fa_fwd_decode_weights(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), None if lengths is None else lengths.data_ptr(),
+            None if weights is None else weights.data_ptr(), wo.data_ptr(), o.data_ptr(), ls.data_ptr(), B, Hq, Hkv,
+            Nq, Nk, d, 1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
+            _stream_handle(None)), "fa_fwd_decode_weights")
+        return o, ls, wo
+
+    return call.run(body)
 
 
 def attention_key_weights(q, k, lse, weights=None, lengths=None, causal=False, scale=None, weights_out=None,
@@ -513,21 +529,29 @@ def attention_key_weights(q, k, lse, weights=None, lengths=None, causal=False, s
     whose lse [B,Hq,Nq] is known, added to weights (fp32 [B,Hkv,Nk]; None:
     zero); see fa_key_weights.  Returns weights_out."""
     call = _CacheCall("attention_key_weights", q, stream)
-    B, Hq, Nq, d, Hkv, Nk = _cache_dims(call, q, k)
-    call.check("q", q, (B, Hq, Nq, d), torch.bfloat16)
-    call.check("k", k, (B, Hkv, Nk, d), torch.bfloat16)
-    call.check("lse", lse, (B, Hq, Nq), torch.float32)
+    B, Hq, Nq, d, Hkv, Nk = call.dims(q, k)
+    check = call.check
+    check("q", q, (B, Hq, Nq, d), torch.bfloat16)
+    check("k", k, (B, Hkv, Nk, d), torch.bfloat16)
+    check("lse", lse, (B, Hq, Nq), torch.float32)
     if weights is not None:
-        call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+        check("weights", weights, (B, Hkv, Nk), torch.float32)
     if lengths is not None:
-        call.check("lengths", lengths, (B,), torch.int32)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with call.scope:
-        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
-        workspace = call.scratch(workspace, fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
-        _check(fa_key_weights(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale,
-                              workspace, workspace.numel() * workspace.element_size()), "fa_key_weights")
-    return weights_out
+        check("lengths", lengths, (B,), torch.int32)
+
+    def body():
+        wo = q.new_empty((B, Hkv, Nk), dtype=torch.float32) if weights_out is None else weights_out
+        if weights_out is not None:
+            check("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
+        ws = call.scratch(workspace, q, lib().fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        _check(lib().fa_key_weights(
+            q.data_ptr(), k.data_ptr(), lse.data_ptr(), None if lengths is None else lengths.data_ptr(),
+            None if weights is None else weights.data_ptr(), wo.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
+            1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
+            _stream_handle(None)), "fa_key_weights")
+        return wo
+
+    return call.run(body)
 
 
 def cache_evict(k, v, weights, budget, recent=0, lengths=None, out_cap=None, k_out=None, v_out=None, weights_out=None,
@@ -542,20 +566,33 @@ def cache_evict(k, v, weights, budget, recent=0, lengths=None, out_cap=None, k_o
     if k.dim() != 4:
         call.refuse("k must be [B, Hkv, Nk, d]")
     B, Hkv, Nk, d = k.shape
-    for name, t in (("k", k), ("v", v)):
-        call.check(name, t, (B, Hkv, Nk, d), torch.bfloat16)
-    call.check("weights", weights, (B, Hkv, Nk), torch.float32)
+    check = call.check
+    check("k", k, (B, Hkv, Nk, d), torch.bfloat16)
+    check("v", v, (B, Hkv, Nk, d), torch.bfloat16)
+    check("weights", weights, (B, Hkv, Nk), torch.float32)
     if lengths is not None:
-        call.check("lengths", lengths, (B,), torch.int32)
-    out_cap = budget if out_cap is None else out_cap
-    if not 1 <= budget <= out_cap or not 0 <= recent <= budget:
+        check("lengths", lengths, (B,), torch.int32)
+    cap = budget if out_cap is None else out_cap
+    if not 1 <= budget <= cap or not 0 <= recent <= budget:
         call.refuse("budget must be in 1 .. out_cap and recent in 0 .. budget")
-    with call.scope:
-        k_out = call.given_or_new("k_out", k_out, (B, Hkv, out_cap, d), torch.bfloat16)
-        v_out = call.given_or_new("v_out", v_out, (B, Hkv, out_cap, d), torch.bfloat16)
-        weights_out = call.given_or_new("weights_out", weights_out, (B, Hkv, out_cap), torch.float32)
-        index = call.given_or_new("index", index, (B, Hkv, out_cap), torch.int32)
-        lengths_out = call.given_or_new("lengths_out", lengths_out, (B,), torch.int32)
-        _check(fa_cache_evict(k, v, weights, lengths, k_out, v_out, weights_out, index, lengths_out, B, Hkv, Nk,
-                              out_cap, budget, recent, d), "fa_cache_evict")
-    return k_out, v_out, weights_out, index, lengths_out
+    rows, slots = (B, Hkv, cap, d), (B, Hkv, cap)
+
+    def given_or_new(name, t, shape, dtype):
+        if t is None:
+            return k.new_empty(shape, dtype=dtype)
+        check(name, t, shape, dtype)
+        return t
+
+    def body():
+        ko = given_or_new("k_out", k_out, rows, torch.bfloat16)
+        vo = given_or_new("v_out", v_out, rows, torch.bfloat16)
+        wo = given_or_new("weights_out", weights_out, slots, torch.float32)
+        io = given_or_new("index", index, slots, torch.int32)
+        lo = given_or_new("lengths_out", lengths_out, (B,), torch.int32)
+        _check(lib().fa_cache_evict(
+            k.data_ptr(), v.data_ptr(), weights.data_ptr(), None if lengths is None else lengths.data_ptr(),
+            ko.data_ptr(), vo.data_ptr(), wo.data_ptr(), io.data_ptr(), lo.data_ptr(), B, Hkv, Nk, cap, budget, recent,
+            d, _stream_handle(None)), "fa_cache_evict")
+        return ko, vo, wo, io, lo
+
+    return call.run(body)
