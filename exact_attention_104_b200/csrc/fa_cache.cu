@@ -261,8 +261,9 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, f
     // memory; the split kernel, launched before that one ends, gets the others.
     // Shares by the SM time that each was measured to take (us): a key tile there,
     // a step here; how full the caches are only the device knows: two thirds.
-    // One after the other, each on all SMs: 32 sequences behind 8192 keys (d 128)
-    // 41 us instead of BATCH, 24 x 5 rows behind 20001 keys (d 256) 125 instead of DRAFT.
+    // Measured against one after the other, each on all SMs: 37 us for 41 (32
+    // sequences behind 8192 keys, d 128), 124 for 125 (24 x 5 rows behind 20001 keys,
+    // d 256, where both are bound by what they can have in flight).
     const double tile_us = D == 64 ? 1.3 : (D == 128 ? 1.8 : 3.2), step_us = D == 64 ? 0.28 : (D == 128 ? 0.56 : 0.39);
     const double cost_t = tile_us * lt.prefix_units * tiles(lt, p.Np);
     const double cost_w = step_us * p.B * p.Hkv * tiles(lw, p.Ncap) * 2 / 3;
