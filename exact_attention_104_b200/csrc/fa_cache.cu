@@ -233,18 +233,21 @@ CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bo
     pl.t_ml = take(rows * 8);
     pl.t_range = take((size_t)pl.units_t * sizeof(int2));
   }
-  // up to 16 rows: their scores are kept (4 bytes a row and key) and turned into
-  // weights; more: the keys are read once more by the kernel for known LSE
-  // (2d bytes a key), which is less than keeping and reading back 16 scores
-  pl.scores = weights && !pl.tc_o;
-  pl.key_weights = weights && pl.tc_o;
-  if (pl.scores) pl.score_off = take((size_t)B * Hkv * R * ((Ncap + 31) / 32 * 32) * 4);
+  // Few rows: their scores are kept (4 bytes a row and key, written and read once)
+  // and turned into weights by the kernel that joins the results.  More rows, or
+  // scores that L2 does not hold: the keys are read once more by the kernel for
+  // known LSE (2d bytes a key).  4 x 8 drafted tokens, 64 rows a kv head, 10007
+  // keys: 31 us with scores, 37 with the second reading.
+  const size_t score_bytes = (size_t)B * Hkv * R * (((size_t)Ncap + 127) / 128 * 128) * 4;
+  pl.scores = weights && (!pl.tc_o || (R <= fa::kCacheScoreRows && score_bytes <= (size_t)64 << 20));
+  pl.key_weights = weights && !pl.scores;
+  if (pl.scores) pl.score_off = take(score_bytes);
   if (pl.key_weights) pl.keyw_off = take(key_weights_plan(B, Hq, Hkv, Nq, Ncap, d).total());
   return pl;
 }
 
 template <int D>
-fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, fa::CacheList lw, fa::CacheList lt,
+fa_status launch_cache(const CUtensorMap (&maps)[4], fa::CacheParams p, fa::CacheList lw, fa::CacheList lt,
                        bool tc_p, bool tc_o, cudaStream_t s) {
   using W = fa::CacheCfg<D>;
   using T = fa::CacheTcCfg<D>;
@@ -291,7 +294,10 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], const fa::CacheParams& p, f
     }
   }
   const unsigned combine = (unsigned)(((long long)p.B * p.Hq * p.Nq + 7) / 8);
-  const unsigned per = p.weights_out ? (unsigned)((p.Ncap + fa::kCacheWeightKeys - 1) / fa::kCacheWeightKeys) : 0;
+  // weights: 4 x 2 caches of 10007 keys, 64 rows: 22 us with 2048 keys a CTA, 11 with 256
+  auto per_unit = [&](int keys) { return p.weights_out ? (unsigned)((p.Ncap + keys - 1) / keys) : 0u; };
+  p.few = (unsigned)(p.B * p.Hkv) * per_unit(fa::kCacheWeightKeys) < 2 * kSms;
+  const unsigned per = per_unit(p.few ? fa::kCacheWeightKeysFew : fa::kCacheWeightKeys);
   const unsigned ctas = combine + (unsigned)(p.B * p.Hkv) * per;
   if (ctas > 0) fa::fa_cache_finish_kernel<D><<<ctas, 256, 0, s>>>(p, tc_p ? lt : lw, tc_o ? lt : lw, combine);
   return launched();
@@ -357,7 +363,8 @@ fa_status cache_decode(const void* q, const void* kp, const void* vp, const void
   p.M = B * p.R;
   p.Np = Np;
   p.Ncap = Ncap;
-  p.cap_pad = (Ncap + 31) / 32 * 32;
+  p.cap_pad = (int)pad128(Ncap);
+  p.wide = Ncap % 4 == 0 && aligned16(weights) && aligned16(weights_out);
   p.causal = causal != 0;
   p.scale_log2 = scale * fa::kLog2e;
   p.wait_cap = g_wait_cap.load(std::memory_order_relaxed);

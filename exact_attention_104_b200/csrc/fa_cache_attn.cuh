@@ -359,27 +359,32 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// Largest m and the sum of l on its scale over a row's partial results.
-__device__ __forceinline__ void cache_ml(const CacheParts& parts, int lane, float& M, float& L) {
-  M = -INFINITY;
-  L = 0.f;
-  for (int s = lane; s < parts.n; s += 32) M = fmaxf(M, parts.ml(s).x);
-  M = warp_max(M);
-  for (int s = lane; s < parts.n; s += 32) {
+// M + log2 Σ l of a row over its partial results (+inf: it sees no key), by
+// `lanes` neighbouring lanes of a warp (a power of two; all lanes call it).
+__device__ __forceinline__ float cache_lse2(const CacheParts& parts, int lane, int lanes) {
+  float M = -INFINITY, L = 0.f;
+#pragma unroll 4
+  for (int s = lane; s < parts.n; s += lanes) M = fmaxf(M, parts.ml(s).x);
+  for (int off = lanes / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 4
+  for (int s = lane; s < parts.n; s += lanes) {
     const float2 ml = parts.ml(s);
     if (ml.x != -INFINITY) L = fmaf(ex2(ml.x - M), ml.y, L);
   }
-  L = warp_sum(L);
+  for (int off = lanes / 2; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+  return L > 0.f ? M + lg2(L) : INFINITY;
 }
 
-// Keys of a CTA of the weights' part of the finish kernel.
-constexpr int kCacheWeightKeys = 2048;
+// Keys of a CTA of the weights' part of the finish kernel: many, or few with the
+// rows dealt to four groups of its threads where there would be too few CTAs.
+constexpr int kCacheWeightKeys = 2048, kCacheWeightKeysFew = 256;
+constexpr int kCacheScoreRows = 64;  // most rows whose scores are stored
 
 // CTAs 0 .. n_combine−1: O and LSE, one query row a warp; a row that no key is
 // visible to has O = 0 and LSE = −inf.  The CTAs behind them (only with stored
-// scores, R <= 16): weights_out[j] = weights[j] + Σ_r 2^(S'_rj − LSE'_r), one CTA
-// for kCacheWeightKeys keys of a (sequence, kv head); keys at or behind the
-// sequence's length keep their weight.  Each joins the rows' m and l by itself
+// scores): weights_out[j] = weights[j] + Σ_r 2^(S'_rj − LSE'_r), one CTA for p.few ?
+// kCacheWeightKeysFew : kCacheWeightKeys keys of a (sequence, kv head); keys at or
+// behind the sequence's length keep their weight.  Each joins the rows' m and l by itself
 // rather than wait for the others' LSE in a launch of its own.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -448,31 +453,38 @@ __global__ void __launch_bounds__(256)
     return;
   }
 
-  __shared__ float lse2[16];
-  const int per = (p.Ncap + kCacheWeightKeys - 1) / kCacheWeightKeys;
+  __shared__ float lse2[kCacheScoreRows];
+  __shared__ float4 group_sum[4][kCacheWeightKeysFew / 4];
+  const int keys = p.few ? kCacheWeightKeysFew : kCacheWeightKeys;
+  const int per = (p.Ncap + keys - 1) / keys;
   const int unit = (blockIdx.x - n_combine) / per, b = unit / p.Hkv;
-  const int j0 = (blockIdx.x - n_combine) % per * kCacheWeightKeys + 4 * (int)threadIdx.x;
+  // thread = four keys in a row, and with few keys one of four groups of rows
+  const int group = p.few ? threadIdx.x / (kCacheWeightKeysFew / 4) : 0, n_group = p.few ? 4 : 1;
+  const int quad = p.few ? threadIdx.x % (kCacheWeightKeysFew / 4) : threadIdx.x;
+  const int j0 = (blockIdx.x - n_combine) % per * keys + 4 * quad;
   const int len = cache_len(p, b);
   if (len < 0) {  // this sequence's weights stay as they are
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
     return;
   }
-  for (int r = warp; r < p.R; r += 8) {
-    float M, L;
-    cache_ml(cache_parts(p, lp, lo, b, unit % p.Hkv, r, len), lane, M, L);
+  {
+    const int lanes = p.R <= 16 ? 16 : 4, r = threadIdx.x / lanes;
+    CacheParts parts;
+    parts.n = parts.n_prefix = 0;
+    if (r < p.R) parts = cache_parts(p, lp, lo, b, unit % p.Hkv, r, len);
     // a row without a visible key gives no weight (its scores are −inf)
-    if (lane == 0) lse2[r] = L > 0.f ? M + lg2(L) : INFINITY;
+    const float x = cache_lse2(parts, threadIdx.x % lanes, lanes);
+    if (r < p.R && threadIdx.x % lanes == 0) lse2[r] = x;
   }
   __syncthreads();
-#pragma unroll
-  for (int c = 0; c < kCacheWeightKeys / 1024; ++c) {
+  for (int c = 0; c < (p.few ? 1 : kCacheWeightKeys / 1024); ++c) {
     const int j = j0 + c * 1024;
-    if (j >= p.Ncap) break;
+    if (j >= p.Ncap && !p.few) break;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if (j < len) {  // scores are stored up to a multiple of 16 keys at least
       const float* src = p.scores + (size_t)unit * p.R * p.cap_pad + j;
 #pragma unroll 8
-      for (int r = 0; r < p.R; ++r) {
+      for (int r = group; r < p.R; r += n_group) {
         const float4 s = *reinterpret_cast<const float4*>(src + (size_t)r * p.cap_pad);
         acc[0] += ex2(s.x - lse2[r]);
         acc[1] += ex2(s.y - lse2[r]);
@@ -480,12 +492,34 @@ __global__ void __launch_bounds__(256)
         acc[3] += ex2(s.w - lse2[r]);
       }
     }
+    if (p.few) {
+      group_sum[group][quad] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      __syncthreads();
+      if (group > 0 || j >= p.Ncap) return;
+#pragma unroll
+      for (int g = 1; g < 4; ++g) {
+        const float4 s = group_sum[g][quad];
+        acc[0] += s.x;
+        acc[1] += s.y;
+        acc[2] += s.z;
+        acc[3] += s.w;
+      }
+    }
+    const size_t at = (size_t)unit * p.Ncap + j;
+    if (p.wide && j + 4 <= p.Ncap) {
+      float4 w = p.weights ? *reinterpret_cast<const float4*>(p.weights + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < len) w.x += acc[0];
+      if (j + 1 < len) w.y += acc[1];
+      if (j + 2 < len) w.z += acc[2];
+      if (j + 3 < len) w.w += acc[3];
+      *reinterpret_cast<float4*>(p.weights_out + at) = w;
+      continue;
+    }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (j + t >= p.Ncap) continue;
-      const size_t at = (size_t)unit * p.Ncap + j + t;
-      const float w = p.weights ? p.weights[at] : 0.f;
-      p.weights_out[at] = j + t < len ? w + acc[t] : w;
+      const float w = p.weights ? p.weights[at + t] : 0.f;
+      p.weights_out[at + t] = j + t < len ? w + acc[t] : w;
     }
   }
 }

@@ -31,7 +31,9 @@ struct CacheParams {
   const float* weights;    // [B, Hkv, Ncap] or null
   float* weights_out;
   int B, Hq, Hkv, G, Nq, R, M;  // R = G·Nq, M = B·R
-  int Np, Ncap, cap_pad;        // cap_pad: Ncap rounded up to 32
+  int Np, Ncap, cap_pad;        // cap_pad: Ncap rounded up to 128
+  int wide;  // the weights can be moved 16 bytes at a time
+  int few;   // fewer keys for each CTA that joins them
   int causal;
   float scale_log2;
   long long wait_cap;

@@ -266,6 +266,13 @@ __global__ void __launch_bounds__(CacheTcCfg<D>::THREADS, 1)
             for (int c = 0; c < 64; ++c)
               if (key0 + c > row_last) s[c] = -INFINITY;
           }
+          if (p.scores && !run.prefix && m < rows) {
+            float4* dst = reinterpret_cast<float4*>(
+                p.scores + ((size_t)(run.b * p.Hkv + run.hkv) * p.R + m) * p.cap_pad + key0);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              dst[c] = make_float4(s[4 * c] * sl2, s[4 * c + 1] * sl2, s[4 * c + 2] * sl2, s[4 * c + 3] * sl2);
+          }
           float a[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

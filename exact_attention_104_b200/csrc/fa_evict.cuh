@@ -132,15 +132,15 @@ __device__ __forceinline__ void evict_select(EvictShared& sh, const float* w, in
   int above = 0;          // greater than every value with this prefix
   int gt = 0, eq = 0;     // of this thread's bins: greater than the threshold, equal to it
   for (int e = tid; e < kEvictBins; e += kEvictThreads) sh.acc[0][e] = 0;
+  if (nrank > 1) cluster_sync();  // every CTA has started, and the sums are clear
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
     for (int e = tid; e < kEvictBins; e += kEvictThreads) {
       sh.hist[e] = 0;
-      sh.acc[(pass + 1) & 1][e] = 0;  // the next pass's
+      sh.acc[(pass + 1) & 1][e] = 0;  // the next pass's; cleared before its first addition by two cluster barriers
     }
-    if (nrank > 1) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     each([&](int bt, const uint32_t* u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
