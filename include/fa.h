@@ -245,14 +245,16 @@ fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, const void*
  * call's *_workspace_bytes function gives; 0 for invalid sizes) is scratch
  * that is in use until the call's kernels have finished, its contents on entry
  * do not matter.  Results do not depend on timing: the same inputs give the
- * same bits.  Other errors as for fa_fwd; B == 0 is a no-op, and Nq == 0 leaves
- * weights_out equal to weights and writes nothing else.
+ * same bits.  Other errors as for fa_fwd (FA_ERR_UNSUPPORTED also where a call
+ * with weights has B * Hkv > 65535, or one would take 2^31 key tiles or more);
+ * B == 0 is a no-op, and Nq == 0 leaves weights_out equal to weights and writes
+ * nothing else.
  *
  * Decoding for a batch that shares a prefix: sequence b is the Np keys of the
  * prefix (k_prefix, v_prefix: bf16 [Hkv, Np, d], one copy for the batch)
  * followed by its own lengths[b] keys out of k, v [B, Hkv, Ncap, d], so
- * L = Np + lengths[b].  The prefix is read once for all sequences' rows rather
- * than once for each.  Np == 0 (k_prefix, v_prefix may be NULL) is decoding
+ * L = Np + lengths[b].  The prefix is read once for each tile of the B * Hq/Hkv * Nq
+ * query rows of a kv head (16 or 128 rows), not once for each sequence.  Np == 0 (k_prefix, v_prefix may be NULL) is decoding
  * over ragged caches; Ncap == 0 (k, v may be NULL) decoding over the prefix
  * alone.  q, o bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] (natural log);
  * Nq <= 256.  The softmax is put together from the key runs' partial results

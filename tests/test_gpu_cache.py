@@ -504,6 +504,51 @@ def test_call_on_a_stream_of_its_own():
     _ok()
 
 
+def test_workspace_given_and_used_again():
+    g = _gen(71)
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")  # its contents do not matter
+    for B, Nq, n in ((2, 1, 300), (3, 9, 77), (2, 1, 300)):
+        q, k, v = _normal(g, B, 4, Nq, 64), _normal(g, B, 2, n, 64), _normal(g, B, 2, n, 64)
+        kp = _normal(g, 2, 200, 64)
+        for call in (lambda **kw: attention_decode_prefix(q, kp, kp, k, v, causal=True, **kw),
+                     lambda **kw: attention_decode_weights(q, k, v, causal=True, **kw)):
+            want = call()
+            assert _same(want, call(workspace=ws))
+            ws.random_(generator=g)
+    _ok()
+
+
+def test_cache_of_more_than_2_to_31_elements():
+    # the last kv head lies behind element 2^31; the others hold zeros
+    Hkv, n, d, budget, recent = 5, 2_000_003, 256, 1000, 100
+    g = _gen(81)
+    k = torch.zeros(1, Hkv, n, d, dtype=BF16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() - n * d < 2 ** 31 < k.numel()
+    k[0, -1], v[0, -1] = _normal(g, n, d), _normal(g, n, d)
+    q = _normal(g, 1, 2 * Hkv, 1, d, std=4.0)
+    o, lse, w = attention_decode_weights(q, k, v, causal=True)
+    kp = _normal(g, Hkv, 40, d)
+    o2, lse2 = attention_decode_prefix(q, kp, kp, k, v, causal=True)
+    w2 = attention_key_weights(q, k, lse, causal=True)
+    ev = cache_evict(k, v, w, budget, recent)
+    _ok()
+    for got_o, got_lse, keys, values in ((o, lse, k[0, -1:], v[0, -1:]),
+                                         (o2, lse2, torch.cat([kp[-1:], k[0, -1:]], 1),
+                                          torch.cat([kp[-1:], v[0, -1:]], 1))):
+        r = ref.attention(q[0, -2:], keys, values, True, 1 / math.sqrt(d))
+        ref.check_o_lse(got_o[0, -2:], got_lse[0, -2:], r, keys.shape[1], "last head")
+        if got_o is o:
+            zero = torch.zeros(1, n, device="cuda")
+            ref.check_weights(w[0, -1:], zero, r, n, False, "decode")
+            ref.check_weights(w2[0, -1:], zero, r, n, True, "key weights")
+        del r
+    order = torch.sort(w[0, -1, :n - recent], descending=True, stable=True).indices[:budget - recent]
+    want = torch.cat([order.sort().values, torch.arange(n - recent, n, device="cuda")])
+    assert torch.equal(ev[3][0, -1].long(), want)
+    assert torch.equal(ev[0][0, -1], k[0, -1, want]) and torch.equal(ev[1][0, -1], v[0, -1, want])
+
+
 # ------------------------------------------------------- refusals, bad data
 @pytest.mark.parametrize("bad", [-1, 301, 2 ** 31 - 1, -2 ** 31])
 def test_lengths_out_of_range_are_reported(bad):
