@@ -8,6 +8,7 @@ library is missing or the device is unsupported, calls raise ``FAError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -392,13 +393,13 @@ class _CacheCall:
     current stream), from whose memory pool the tensors it allocates come.
     ``scope`` is None where that is the state already."""
 
-    __slots__ = ("where", "device", "index", "scope")
+    __slots__ = ("where", "first", "index", "scope")
 
     def __init__(self, where, first, stream):
         self.where = where
+        self.first = first
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             self.refuse("inputs must be CUDA tensors")
-        self.device = first.device
         self.index = first.get_device()
         self.scope = None
         if stream is not None:
@@ -409,14 +410,18 @@ class _CacheCall:
             if stream.device != self.device:
                 self.refuse("the stream belongs to another device")
             self.scope = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != self.index:
+        elif torch._C._cuda_getDevice() != self.index:
             self.scope = torch.cuda.device(self.device)
+
+    @property
+    def device(self):
+        return self.first.device
 
     def refuse(self, why):
         raise FAError(FA_ERR_INVALID_ARG, f"{self.where}: {why}")
 
     def check(self, name, t, shape, dtype):
-        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.index
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == self.index and t.shape == shape
                 and t.is_contiguous()):
             return
         if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
@@ -424,10 +429,10 @@ class _CacheCall:
         self.refuse(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)} "
                     f"with strides {list(t.stride())}")
 
-    def scratch(self, t, first, need):
+    def scratch(self, t, need):
         """The caller's workspace, or a new one of the size needed."""
         if t is None:
-            return first.new_empty(max(need, 256), dtype=torch.uint8)
+            return self.first.new_empty(max(need, 256), dtype=torch.uint8)
         if not isinstance(t, torch.Tensor) or t.get_device() != self.index or not t.is_contiguous():
             self.refuse(f"workspace must be a contiguous tensor on {self.device}")
         return t
@@ -439,9 +444,15 @@ class _CacheCall:
 
     def run(self, body):
         if self.scope is None:
-            return body()
+            return body(torch._C._cuda_getCurrentRawStream(self.index))
         with self.scope:
-            return body()
+            return body(torch._C._cuda_getCurrentRawStream(self.index))
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, *sizes):
+    """A workspace query, a pure function of the sizes."""
+    return getattr(lib(), name)(*sizes)
 
 
 def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lengths=None, causal=False, scale=None, out=None, lse=None,
@@ -465,19 +476,19 @@ def attention_decode_prefix(q, k_prefix, v_prefix, k, v, lengths=None, causal=Fa
     if lengths is not None:
         check("lengths", lengths, (B,), torch.int32)
 
-    def body():
+    def body(handle):
         o = torch.empty_like(q) if out is None else out
         ls = q.new_empty((B, Hq, Nq), dtype=torch.float32) if lse is None else lse
         if out is not None:
             check("out", out, (B, Hq, Nq, d), torch.bfloat16)
         if lse is not None:
             check("lse", lse, (B, Hq, Nq), torch.float32)
-        ws = call.scratch(workspace, q, lib().fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ncap, d))
+        ws = call.scratch(workspace, _workspace_bytes("fa_decode_prefix_workspace_bytes", B, Hq, Hkv, Nq, Np, Ncap, d))
         _check(lib().fa_fwd_decode_prefix(
             q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(),
             None if lengths is None else lengths.data_ptr(), o.data_ptr(), ls.data_ptr(), B, Hq, Hkv, Nq, Np, Ncap, d,
             1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
-            _stream_handle(None)), "fa_fwd_decode_prefix")
+            handle), "fa_fwd_decode_prefix")
         return o, ls
 
     return call.run(body)
@@ -501,7 +512,7 @@ def attention_decode_weights(q, k, v, weights=None, lengths=None, causal=False, 
     if lengths is not None:
         check("lengths", lengths, (B,), torch.int32)
 
-    def body():
+    def body(handle):
         o = torch.empty_like(q) if out is None else out
         ls = q.new_empty((B, Hq, Nq), dtype=torch.float32) if lse is None else lse
         wo = q.new_empty((B, Hkv, Nk), dtype=torch.float32) if weights_out is None else weights_out
@@ -511,12 +522,12 @@ def attention_decode_weights(q, k, v, weights=None, lengths=None, causal=False, 
             check("lse", lse, (B, Hq, Nq), torch.float32)
         if weights_out is not None:
             check("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
-        ws = call.scratch(workspace, q, lib().fa_decode_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        ws = call.scratch(workspace, _workspace_bytes("fa_decode_weights_workspace_bytes", B, Hq, Hkv, Nq, Nk, d))
         _check(lib().fa_fwd_decode_weights(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), None if lengths is None else lengths.data_ptr(),
             None if weights is None else weights.data_ptr(), wo.data_ptr(), o.data_ptr(), ls.data_ptr(), B, Hq, Hkv,
             Nq, Nk, d, 1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
-            _stream_handle(None)), "fa_fwd_decode_weights")
+            handle), "fa_fwd_decode_weights")
         return o, ls, wo
 
     return call.run(body)
@@ -539,16 +550,16 @@ def attention_key_weights(q, k, lse, weights=None, lengths=None, causal=False, s
     if lengths is not None:
         check("lengths", lengths, (B,), torch.int32)
 
-    def body():
+    def body(handle):
         wo = q.new_empty((B, Hkv, Nk), dtype=torch.float32) if weights_out is None else weights_out
         if weights_out is not None:
             check("weights_out", weights_out, (B, Hkv, Nk), torch.float32)
-        ws = call.scratch(workspace, q, lib().fa_key_weights_workspace_bytes(B, Hq, Hkv, Nq, Nk, d))
+        ws = call.scratch(workspace, _workspace_bytes("fa_key_weights_workspace_bytes", B, Hq, Hkv, Nq, Nk, d))
         _check(lib().fa_key_weights(
             q.data_ptr(), k.data_ptr(), lse.data_ptr(), None if lengths is None else lengths.data_ptr(),
             None if weights is None else weights.data_ptr(), wo.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
             1 if causal else 0, d ** -0.5 if scale is None else scale, ws.data_ptr(), ws.nbytes,
-            _stream_handle(None)), "fa_key_weights")
+            handle), "fa_key_weights")
         return wo
 
     return call.run(body)
@@ -583,7 +594,7 @@ def cache_evict(k, v, weights, budget, recent=0, lengths=None, out_cap=None, k_o
         check(name, t, shape, dtype)
         return t
 
-    def body():
+    def body(handle):
         ko = given_or_new("k_out", k_out, rows, torch.bfloat16)
         vo = given_or_new("v_out", v_out, rows, torch.bfloat16)
         wo = given_or_new("weights_out", weights_out, slots, torch.float32)
@@ -592,7 +603,7 @@ def cache_evict(k, v, weights, budget, recent=0, lengths=None, out_cap=None, k_o
         _check(lib().fa_cache_evict(
             k.data_ptr(), v.data_ptr(), weights.data_ptr(), None if lengths is None else lengths.data_ptr(),
             ko.data_ptr(), vo.data_ptr(), wo.data_ptr(), io.data_ptr(), lo.data_ptr(), B, Hkv, Nk, cap, budget, recent,
-            d, _stream_handle(None)), "fa_cache_evict")
+            d, handle), "fa_cache_evict")
         return ko, vo, wo, io, lo
 
     return call.run(body)
