@@ -265,13 +265,23 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], fa::CacheParams p, fa::Cach
     // Shares by the SM time that each was measured to take (us): a key tile there,
     // a step here; how full the caches are only the device knows: two thirds.
     // Measured against one after the other, each on all SMs: 37 us for 41 (32
-    // sequences behind 8192 keys, d 128), 124 for 125 (24 x 5 rows behind 20001 keys,
-    // d 256, where both are bound by what they can have in flight).
+    // sequences behind 8192 keys, d 128); 24 x 5 rows behind 20001 keys (d 256): 124
+    // for 125, with the row tiles in step (below) 105.
     const double tile_us = D == 64 ? 1.3 : (D == 128 ? 1.8 : 3.2), step_us = D == 64 ? 0.28 : (D == 128 ? 0.56 : 0.39);
     const double cost_t = tile_us * lt.prefix_units * tiles(lt, p.Np);
     const double cost_w = step_us * p.B * p.Hkv * tiles(lw, p.Ncap) * 2 / 3;
     lt.n_ctas = std::min(kSms - 8, std::max(8, (int)(kSms * cost_t / (cost_t + cost_w) + 0.5)));
+    if (lt.prefix_rt > 1 && lt.prefix_units < kSms - 8)  // see below
+      lt.n_ctas = std::min((kSms - 8) / lt.prefix_units,
+                           std::max(1, (lt.n_ctas + lt.prefix_units / 2) / lt.prefix_units)) * lt.prefix_units;
     lw.n_ctas = (kSms - lt.n_ctas) * W::PER_SM;
+  }
+  // Several row tiles of a prefix read the same K and V: where the same number of
+  // CTAs for every unit uses nearly all CTAs, the tiles go in step and L2 serves
+  // all but the first.
+  if (lt.prefix_rt > 1 && lt.own_rt == 0) {
+    const int split = lt.n_ctas / lt.prefix_units;
+    if (10 * split * lt.prefix_units >= 9 * lt.n_ctas) lt.split = split;
   }
   if (have_t) {
     auto kern = fa::fa_cache_tc_kernel<D>;

@@ -48,6 +48,7 @@ struct CacheList {
   int prefix_rt;     // row tiles of the prefix's M rows
   int own_rt;        // row tiles of a sequence's R rows; 0: own keys are not in this list
   int n_ctas;
+  int split;         // prefix only: CTAs a unit, so that the row tiles read the same keys at the same time; 0: equal runs
   float* part_o;     // [slots][rows][d]
   float* part_ml;    // [slots][rows][2]: m (log2 units), l
   int2* range;       // [units] first and last CTA
@@ -105,6 +106,16 @@ struct CacheRuns {
   // refuses lists of 2^31 - 2^20 key tiles and more.)
   __device__ __forceinline__ bool start(const CacheParams& p, const CacheList& l, int cta) {
     const int lane = threadIdx.x & 31;
+    if (l.split > 0) {  // `split` CTAs a unit
+      unit = cta / l.split;
+      if (unit >= l.prefix_units) return false;
+      set_prefix(p, l);
+      const int per = (tiles + l.split - 1) / l.split;
+      t0 = (cta - unit * l.split) * per;
+      left = min(per, tiles - t0);
+      set_end();
+      return left > 0;
+    }
     const int in_prefix = l.prefix_units > 0 ? l.prefix_units * tiles_of(l, p.Np) : 0;
     // 32 sequences at a time: their tiles and the sum up to each; the first 32
     // (mostly all) are needed twice and stay

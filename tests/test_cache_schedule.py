@@ -130,6 +130,27 @@ def _cache_runs(p_units, p_rt, np_keys, Hkv, own_rt, lens, keys, n_ctas, cta):
         unit = p_units + (b * Hkv + hkv) * own_rt + rt
 
 
+@pytest.mark.parametrize("units,tiles,n_ctas", [(16, 157, 96), (6, 1, 148), (24, 3, 144), (5, 7, 25), (2, 300, 148)])
+def test_cache_work_list_of_a_prefix_in_step(units, tiles, n_ctas):
+    """The same number of CTAs for every unit: every tile once, no gap between a
+    unit's first and last CTA, slots of their own."""
+    split = n_ctas // units
+    per, seen, slots, ctas = -(-tiles // split), set(), set(), {}
+    for cta in range(n_ctas):
+        unit = cta // split
+        t0 = (cta - unit * split) * per
+        if unit >= units or t0 >= tiles:
+            continue
+        for t in range(t0, min(tiles, t0 + per)):
+            assert (unit, t) not in seen
+            seen.add((unit, t))
+        assert unit + cta not in slots
+        slots.add(unit + cta)
+        ctas.setdefault(unit, []).append(cta)
+    assert len(seen) == units * tiles and max(slots) < units + n_ctas
+    assert all(c == list(range(c[0], c[-1] + 1)) for c in ctas.values())
+
+
 @pytest.mark.parametrize("seed", range(60))
 def test_cache_work_list(seed):
     rng = random.Random(seed)
