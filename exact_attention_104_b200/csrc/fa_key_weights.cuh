@@ -94,7 +94,7 @@ struct KeyWCfg {
   // buffers of the rows' −LSE and of the steps' KeyWStep.  A wait by parity must
   // not run a phase ahead: with a multiple of 2 and of NWG, a buffer has one
   // filling warp and the same reading warpgroups every time
-  static constexpr int NL = 4;
+  static constexpr int NL = 8;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = NK * KTILE;
   static constexpr int LSE_OFF = Q_OFF + NQ * QTILE;
@@ -372,43 +372,47 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
     const uint64_t dk = sdesc_sw128(sbase + C::K_OFF, 16, 1024);
     const uint64_t dq = sdesc_sw128(sbase + C::Q_OFF, 16, 1024);
     int kseq = 0, qseq = 0, sub = 0;  // first K tile of the unit, Q tile (resident: the group's first), product
-    bool new_unit = true, new_head = true, ok = true;
+    bool new_head = true, ok = true;
     while (true) {
+      // a unit at a time: what its steps have in common is off their path
       if (RESIDENT && new_head)
         for (int s = 0; s < p.row_tiles && ok; ++s)
           ok = mbar_wait_warp(BAR(C::B_QFULL + (qseq + s) % C::NQ), ((qseq + s) / C::NQ) & 1, wc, 35);
-      if (new_unit)
-        for (int k = 0; k < C::KU && ok; ++k)
-          ok = mbar_wait_warp(BAR(C::B_KFULL + (kseq + k) % C::NK), ((kseq + k) / C::NK) & 1, wc, 36);
-      if (!RESIDENT && ok) ok = mbar_wait_warp(BAR(C::B_QFULL + qseq % C::NQ), (qseq / C::NQ) & 1, wc, 35);
-      if (!ok) break;
-      const uint32_t qoff = (RESIDENT ? (qseq + it.s) % C::NQ : qseq % C::NQ) * C::QTILE;
+      for (int k = 0; k < C::KU && ok; ++k)
+        ok = mbar_wait_warp(BAR(C::B_KFULL + (kseq + k) % C::NK), ((kseq + k) / C::NK) & 1, wc, 36);
+      const int m = min(it.left, it.n - it.s);  // steps of the unit here
+      for (int e = 0; e < m && ok; ++e) {
+        const int qs = RESIDENT ? qseq + it.s + e : qseq;
+        if (!RESIDENT) ok = mbar_wait_warp(BAR(C::B_QFULL + qs % C::NQ), (qs / C::NQ) & 1, wc, 35);
+        const uint32_t qoff = qs % C::NQ * C::QTILE;
 #pragma unroll
-      for (int k = 0; k < C::KU; ++k) {
-        const int x = sub % C::NBUF;
-        if (!mbar_wait_warp(BAR(C::B_SEMPTY + x), ((sub / C::NBUF) & 1) ^ 1, wc, 37)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t koff = (kseq + k) % C::NK * C::KTILE;
+        for (int k = 0; k < C::KU; ++k) {
+          const int x = sub % C::NBUF;
+          ok = ok && mbar_wait_warp(BAR(C::B_SEMPTY + x), ((sub / C::NBUF) & 1) ^ 1, wc, 37);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t koff = (kseq + k) % C::NK * C::KTILE;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss_w(tbase + x * C::BN, sdesc_add(dk, koff + (kk >> 2) * C::KPANEL + (kk & 3) * 32),
-                   sdesc_add(dq, qoff + (kk >> 2) * C::QPANEL + (kk & 3) * 32), C::IDESC, kk > 0 ? 1u : 0u);
-        tc_commit_w(BAR(C::B_SFULL + x));
-        ++sub;
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_w(tbase + x * C::BN, sdesc_add(dk, koff + (kk >> 2) * C::KPANEL + (kk & 3) * 32),
+                     sdesc_add(dq, qoff + (kk >> 2) * C::QPANEL + (kk & 3) * 32), C::IDESC, kk > 0 ? 1u : 0u);
+          tc_commit_w(BAR(C::B_SFULL + x));
+          ++sub;
+        }
+        if (!RESIDENT) {
+          tc_commit_w(BAR(C::B_QEMPTY + qs % C::NQ));
+          ++qseq;
+        }
       }
       if (!ok) break;
-      new_unit = it.unit_ends();
+      it.left -= m - 1;
+      it.s += m - 1;
       new_head = it.head_ends();
-      if (!RESIDENT) {
-        tc_commit_w(BAR(C::B_QEMPTY + qseq % C::NQ));
-        ++qseq;
-      } else if (new_head) {
+      for (int k = 0; k < C::KU; ++k) tc_commit_w(BAR(C::B_KEMPTY + (kseq + k) % C::NK));
+      kseq += C::KU;
+      if (RESIDENT && new_head) {
         for (int s = 0; s < p.row_tiles; ++s) tc_commit_w(BAR(C::B_QEMPTY + (qseq + s) % C::NQ));
         qseq += p.row_tiles;
-      }
-      if (new_unit) {
-        for (int k = 0; k < C::KU; ++k) tc_commit_w(BAR(C::B_KEMPTY + (kseq + k) % C::NK));
-        kseq += C::KU;
       }
       if (it.left == 1) break;
       it.next(p);
@@ -418,22 +422,39 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
     mbar_wait_inflight(BAR(C::B_DRAIN), 0, wc, 38);
   } else if (warp < 4) {
     KeyWStep* steps = reinterpret_cast<KeyWStep*>(smem + C::STEP_OFF);
-    int q0 = 0;  // first step of the unit here
+    int q0 = 0;       // first step of the unit here
+    int filled = -1;  // this warp's step whose values are held in `st` and `v`
+    KeyWStep st;
+    float v[C::BN / 32];
+    auto publish = [&]() -> bool {
+      if (filled < 0) return true;
+      const int y = filled % C::NL;
+      if (!mbar_wait_warp(BAR(C::B_LEMPTY + y), ((filled / C::NL) & 1) ^ 1, wc, 39)) return false;
+#pragma unroll
+      for (int c = 0; c < C::BN / 32; ++c) {
+        const float g = -v[c] * kLog2e;
+        lse_s[y * C::BN + c * 32 + lane] = g == INFINITY ? -INFINITY : g;
+      }
+      if (lane == 0) steps[y] = st;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::B_LFULL + y));
+      return true;
+    };
     for (int q = 0;; ++q) {
       const size_t unit = ((size_t)it.b * p.Hkv + it.hkv) * p.units + it.u;
       if ((q & 1) == warp - 2) {
+        // the loads of one step are in flight while the one before is handed over
         const int row0 = it.row0(p), rows = it.rows(p);
         const float* src = p.lse + ((size_t)it.b * p.Hq + it.hkv * p.G) * p.Nq + row0;
-        float v[C::BN / 32];
+        float next[C::BN / 32];
 #pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) {
-          v[c] = -INFINITY;
-          if (c * 32 + lane < rows) {
-            v[c] = -src[c * 32 + lane] * kLog2e;
-            if (v[c] == INFINITY) v[c] = -INFINITY;
-          }
+        for (int c = 0; c < C::BN / 32; ++c) next[c] = c * 32 + lane < rows ? src[c * 32 + lane] : INFINITY;
+        if (!publish()) {
+          filled = -1;
+          break;
         }
-        KeyWStep st;
+#pragma unroll
+        for (int c = 0; c < C::BN / 32; ++c) v[c] = next[c];
         st.rows = rows;
         st.need = p.causal ? it.u * C::KEYS - (it.seq.len - p.Nq) : -C::KEYS;
         st.first = 0;
@@ -442,12 +463,7 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
         st.slot = (int)unit + cta;
         st.keys = it.seq.len - it.u * C::KEYS;
         st.per_head = !it.packed();
-        if (!mbar_wait_warp(BAR(C::B_LEMPTY + q % C::NL), ((q / C::NL) & 1) ^ 1, wc, 39)) break;
-#pragma unroll
-        for (int c = 0; c < C::BN / 32; ++c) lse_s[q % C::NL * C::BN + c * 32 + lane] = v[c];
-        if (lane == 0) steps[q % C::NL] = st;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::B_LFULL + q % C::NL));
+        filled = q;
       }
       if (warp == 2 && lane == 0) {
         if (it.s == 0) p.range[unit].x = cta;
@@ -462,6 +478,7 @@ __global__ void __launch_bounds__(KeyWCfg<D, RESIDENT>::THREADS, 1)
       if (it.left == 1) break;
       it.next(p);
     }
+    publish();
   } else {
     const int grp = (warp - 4) >> 2, quarter = warp & 3;
     const int mykey = quarter * 32 + lane;

@@ -308,7 +308,7 @@ def test_key_weights_protocol(shape):
     resident, nk, nq, nbuf = shape
     for seed in range(12):
         rng = random.Random(seed)
-        _simulate(_units(resident, nq, rng), resident, nk, nq, nbuf, 4, seed)
+        _simulate(_units(resident, nq, rng), resident, nk, nq, nbuf, 8, seed)
 
 
 def test_key_weights_model_catches_a_ring_whose_readers_change():
