@@ -551,6 +551,17 @@ fa_status fa_cache_evict(const void* k, const void* v, const float* weights, con
   p.err = di->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const unsigned units = (unsigned)(B * Hkv);
+  // small caches: one launch, whose one CTA a (sequence, kv head) copies too.  2 x
+  // 1000 weights cut to 256 slots of 128 bytes: 23 us a call from Python for 27 with
+  // two; 64 x 4000 cut to 500 of 256 bytes would take 19 us on the GPU for 14.
+  if (Nk <= fa::kEvictHeld * fa::kEvictBatch && (long long)budget * d <= 1 << 15) {
+    switch (d) {
+      case 64: fa::fa_evict_kernel<64><<<units, fa::kEvictThreads, 0, s>>>(p); break;
+      case 128: fa::fa_evict_kernel<128><<<units, fa::kEvictThreads, 0, s>>>(p); break;
+      default: fa::fa_evict_kernel<256><<<units, fa::kEvictThreads, 0, s>>>(p); break;
+    }
+    return launched();
+  }
   if (evict_select(p, s) != FA_OK) return FA_ERR_CUDA;
   const dim3 grid((unsigned)((budget + fa::kEvictCopyRows - 1) / fa::kEvictCopyRows), units);
   switch (d) {

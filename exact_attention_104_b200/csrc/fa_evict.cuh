@@ -10,6 +10,7 @@
 //                           ordered integers), then one pass that numbers what
 //                           is kept
 //   fa_evict_copy_kernel    gathers K, V and the weights; bound by HBM
+//   fa_evict_kernel         both, for small caches
 //
 // The selection of a (sequence, kv head) is one cluster of CTAs: each counts its
 // share of the weights, and the counts are added up in the first CTA through
@@ -245,15 +246,15 @@ __device__ __forceinline__ void evict_select(EvictShared& sh, const float* w, in
   });
 }
 
-// Grid: units · cluster size; cluster rank r owns the r-th share of the
-// candidates.
-__global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const EvictParams p, int nrank) {
-  __shared__ EvictShared sh;
-  const int rank = blockIdx.x % nrank, unit = blockIdx.x / nrank, b = unit / p.Hkv;
+// Writes the kept indices of one (sequence, kv head), of whose candidates this
+// CTA, `rank` of a cluster of `nrank`, owns its share.  False (for the whole
+// cluster) where the length is out of range and nothing is written.
+__device__ __forceinline__ bool evict_choose(const EvictParams& p, EvictShared& sh, int unit, int rank, int nrank) {
+  const int b = unit / p.Hkv;
   const int n = evict_len(p, b);
-  if (n < 0) {  // nothing of this sequence is written
+  if (n < 0) {
     if (threadIdx.x == 0) atomicCAS(p.err, 0, kDevBadSeqlens);
-    return;  // the same for the whole cluster
+    return false;
   }
   int* index = p.index + (size_t)unit * p.out_cap;
   const int count = min(n, p.budget);
@@ -262,32 +263,28 @@ __global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const Ev
   if (unit % p.Hkv == 0 && gid == 0) p.lengths_out[b] = count;
   if (n <= p.budget) {
     for (int j = gid; j < n; j += all) index[j] = j;
-    return;
+    return true;
   }
   const int nc = n - p.recent, need = p.budget - p.recent;  // candidates, and how many of them stay
   for (int j = gid; j < p.recent; j += all) index[need + j] = nc + j;
-  if (need == 0) return;
+  if (need == 0) return true;
   const float* w = p.weights + (size_t)unit * p.Ncap;
   const int share = (nc + nrank - 1) / nrank;
   const int j0 = min(nc, rank * share), j1 = min(nc, j0 + share);
   if (share <= kEvictHeld * kEvictBatch) evict_select<true>(sh, w, index, need, j0, j1, rank, nrank);
   else evict_select<false>(sh, w, index, need, j0, j1, rank, nrank);
+  return true;
 }
 
-// One thread moves 16 bytes of K and of V at a time; slots count .. budget−1
-// are set to zero, those behind the budget stay as they are.
-constexpr int kEvictCopyRows = 32;  // slots of a CTA
+// Slots r0 .. r1−1 of one (sequence, kv head) by the whole CTA.  One thread moves
+// 16 bytes of K and of V at a time; slots count .. budget−1 are set to zero.
 template <int D>
-__global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictParams p) {
-  const int unit = blockIdx.y, b = unit / p.Hkv;
-  const int n = evict_len(p, b);
-  if (n < 0) return;
+__device__ __forceinline__ void evict_copy(const EvictParams& p, int unit, int r0, int r1) {
   constexpr int CPR = D / 8;  // 16-byte chunks of a row
-  const int r0 = blockIdx.x * kEvictCopyRows, r1 = min(p.budget, r0 + kEvictCopyRows);
   const size_t in0 = (size_t)unit * p.Ncap, out0 = (size_t)unit * p.out_cap;
   const uint4 *k = reinterpret_cast<const uint4*>(p.k), *v = reinterpret_cast<const uint4*>(p.v);
   uint4 *ko = reinterpret_cast<uint4*>(p.k_out), *vo = reinterpret_cast<uint4*>(p.v_out);
-  for (int e = threadIdx.x; e < (r1 - r0) * CPR; e += 256) {
+  for (int e = threadIdx.x; e < (r1 - r0) * CPR; e += blockDim.x) {
     const int r = r0 + e / CPR, c = e % CPR;
     const int src = p.index[out0 + r];
     uint4 a = make_uint4(0, 0, 0, 0), bb = a;
@@ -299,6 +296,30 @@ __global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictParams p)
     vo[(out0 + r) * CPR + c] = bb;
     if (c == 0) p.weights_out[out0 + r] = src >= 0 ? p.weights[in0 + src] : 0.f;
   }
+}
+
+// Grid: units · cluster size.
+__global__ void __launch_bounds__(kEvictThreads) fa_evict_select_kernel(const EvictParams p, int nrank) {
+  __shared__ EvictShared sh;
+  evict_choose(p, sh, blockIdx.x / nrank, blockIdx.x % nrank, nrank);
+}
+
+constexpr int kEvictCopyRows = 32;  // slots of a CTA
+template <int D>
+__global__ void __launch_bounds__(256) fa_evict_copy_kernel(const EvictParams p) {
+  const int unit = blockIdx.y;
+  if (evict_len(p, unit / p.Hkv) < 0) return;
+  const int r0 = blockIdx.x * kEvictCopyRows;
+  evict_copy<D>(p, unit, r0, min(p.budget, r0 + kEvictCopyRows));
+}
+
+// Both in one launch, a CTA for each (sequence, kv head).
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) fa_evict_kernel(const EvictParams p) {
+  __shared__ EvictShared sh;
+  if (!evict_choose(p, sh, blockIdx.x, 0, 1)) return;
+  __syncthreads();
+  evict_copy<D>(p, blockIdx.x, 0, p.budget);
 }
 
 }  // namespace fa
