@@ -35,7 +35,7 @@
 //   warps 4-19    four warpgroups, a 128-key part of a step each in turn;
 //                 thread = key
 //
-// Measured (B200, 8192-token prompt, 16 heads on 4 kv heads, d = 128): 172 us.
+// Measured (B200, 8192-token prompt, 16 heads on 4 kv heads, d = 128): 169 us.
 // The exponentials alone would take 123 us at 1.9 GHz, the product 85 us at
 // 1.63 PFLOP/s; a warpgroup computes 70 % of the time and waits for its next
 // product in most of the rest, since 512 TMEM columns hold one S buffer for

@@ -504,6 +504,37 @@ def test_call_on_a_stream_of_its_own():
     _ok()
 
 
+def test_more_than_32_sequences_and_none_with_a_key():
+    lens = [(37 * b) % 150 for b in range(70)]
+    for some in (lens, [0] * 70):
+        _check_prefix(70, 4, 2, 1, 200, 150, 64, True, some, seed=91)
+        _check_prefix(70, 4, 2, 9, 0, 150, 64, True, some, seed=92)
+        _check_decode_weights(70, 4, 2, 2, 150, 64, True, some, seed=93)
+        _check_decode_weights(70, 8, 1, 9, 150, 128, True, some, seed=94)
+        _check_key_weights(70, 4, 2, 150, 150, 64, True, some, seed=95)
+        _check_key_weights(70, 4, 2, 20, 150, 128, True, some, seed=96)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+@pytest.mark.parametrize("n", [40, 41])
+def test_weights_at_any_4_byte_boundary(shift, n):
+    g = _gen(101)
+    q, k, v = _normal(g, 2, 4, 3, 64), _normal(g, 2, 2, n, 64), _normal(g, 2, 2, n, 64)
+    lens = _lengths([n, 7])
+    buf = torch.rand(2 * 2 * n + 4, generator=g, device="cuda")
+    w = buf[shift:shift + 4 * n].view(2, 2, n)
+    aligned = w.clone()
+    o, lse, want = attention_decode_weights(q, k, v, aligned, lens, causal=True)
+    want2 = attention_key_weights(q, k, lse, aligned, lens, causal=True)
+    got2 = attention_key_weights(q, k, lse, w, lens, causal=True)
+    ev = cache_evict(k, v, aligned, 20, 3, lens), cache_evict(k, v, w, 20, 3, lens)
+    around = buf.clone()
+    _, _, got = attention_decode_weights(q, k, v, w, lens, causal=True, weights_out=w)
+    _ok()
+    assert torch.equal(got, want) and torch.equal(got2, want2) and _same(*ev)
+    assert torch.equal(buf[:shift], around[:shift]) and torch.equal(buf[shift + 4 * n:], around[shift + 4 * n:])
+
+
 def test_workspace_given_and_used_again():
     g = _gen(71)
     ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")  # its contents do not matter
