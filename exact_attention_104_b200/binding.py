@@ -60,6 +60,8 @@ def lib() -> ctypes.CDLL:
     L.fa_selftest_wait_timeout.restype = i
     L.fa_selftest_exp2.argtypes = [vp, vp, ctypes.c_longlong, i, vp]
     L.fa_selftest_exp2.restype = i
+    L.fa_selftest_cache_share.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(i)]
+    L.fa_selftest_cache_share.restype = i
     L.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp]
     L.fa_bwd_noalloc.restype = i
     L.fa_decode_workspace_bytes.argtypes = [i, i, i, i, i, i]
@@ -149,6 +151,14 @@ def fa_bwd(q, k, v, o, lse, do, dq, dk, dv, B, Hq, Hkv, N, d, causal, scale, wor
 
 def fa_selftest_wait_timeout(cap_cycles: int, stream=None) -> int:
     return lib().fa_selftest_wait_timeout(int(cap_cycles), _stream_handle(stream))
+
+
+def fa_selftest_cache_share(B, Hq, Hkv, Nq, Np, Ncap, d) -> tuple[int, int]:
+    """SMs that decoding behind a prefix gives to the prefix, and CTAs of each of
+    its units in step (see fa.h); no GPU is needed."""
+    share = (ctypes.c_int * 2)()
+    _check(lib().fa_selftest_cache_share(B, Hq, Hkv, Nq, Np, Ncap, d, share), "fa_selftest_cache_share")
+    return share[0], share[1]
 
 
 def fa_selftest_exp2(x, y, use_poly: bool, stream=None) -> int:

@@ -246,6 +246,54 @@ CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bo
   return pl;
 }
 
+// How the two attention kernels divide the SMs when both run at once: the prefix's
+// many rows take `n_ctas` of them, `split` CTAs a unit where its row tiles go in
+// step (0: equal runs), the few rows of each sequence the rest.  Modelled time: the
+// slower of the two, the prefix's from its key tiles and changes of unit in a CTA,
+// the other's from its steps.  Measured SM time (us), kernels alone: a tile 1.3, 1.8,
+// 3.2 (d = 64, 128, 256), a unit's start and end 4, 4, 6, a step 0.15, 0.28, 0.33.
+// How full the caches are only the device knows: two thirds.
+//
+// The prefix has 28 SMs at least, which cost the other kernel nothing: 112 to 128 SMs
+// read as much as HBM gives.  It leaves 16, for caches fuller than thought.  240
+// sequences, 64 heads on 8, d 128, 128-key prefix, caches full to 1500 keys: 258 us
+// with 8 SMs for the prefix, 246 with 28, 813 with 120.  160 such sequences, 20001
+// keys, caches of 100: 244 us with 80 SMs, 178 with 132, 227 with 140.
+//
+// Several row tiles of a prefix read the same K and V: in step, L2 serves all but the
+// first, and no CTA has more than one unit.  24 x 5 rows behind 20001 keys (d 256): 107
+// us in step on 96 SMs for 133 in equal runs on 93; 48 x 5 behind 6000: 98 on 64 for
+// 102 on 74.  The model has not that in it, so it may say up to a tenth more.  Beyond
+// that, equal runs: 100 x 2 rows behind 4096 keys (d 128), 72 us on 76 SMs for 80 in
+// step on 56 with caches two thirds full, but 90 for 80 with full ones.
+struct CacheShare {
+  int n_ctas, split;
+};
+CacheShare cache_share(int units, int unit_tiles, int row_tiles, long long steps, int d) {
+  constexpr int kLeast = 28, kMost = kSms - 16;
+  const double tile_us = d == 64 ? 1.3 : (d == 128 ? 1.8 : 3.2), unit_us = d == 256 ? 6 : 4;
+  const double step_us = d == 64 ? 0.15 : (d == 128 ? 0.28 : 0.33);
+  const long long tiles = (long long)units * unit_tiles;
+  const double cost_t = tile_us * tiles + unit_us * units, cost_w = step_us * steps * 2 / 3;
+  auto slower = [&](double prefix_us, int n) { return std::max(prefix_us, cost_w / (kSms - n)); };
+  int n = std::min(kMost, std::max(kLeast, (int)(kSms * cost_t / (cost_t + cost_w) + 0.5)));
+  n = (int)std::min<long long>(n, tiles);
+  CacheShare share{n, 0};
+  if (row_tiles > 1) {
+    const long long run = (tiles + n - 1) / n;  // a CTA's tiles, of so many units at most:
+    double best = 1.1 * slower(run * tile_us + ((run + unit_tiles - 2) / unit_tiles + 1) * unit_us, n);
+    const int most = std::min(std::min(n / units + 1, unit_tiles), kMost / units);
+    for (int split = std::max(1, n / units); split <= most; ++split) {
+      const double us = slower((unit_tiles + split - 1) / split * tile_us + unit_us, split * units);
+      if (us <= best) {
+        best = us;
+        share = CacheShare{split * units, split};
+      }
+    }
+  }
+  return share;
+}
+
 template <int D>
 fa_status launch_cache(const CUtensorMap (&maps)[4], fa::CacheParams p, fa::CacheList lw, fa::CacheList lt,
                        bool tc_p, bool tc_o, cudaStream_t s) {
@@ -262,24 +310,16 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], fa::CacheParams p, fa::Cach
     // once, on SMs of their own, since one is bound by its softmax and the other
     // by reading keys.  The tcgen05 kernel goes first and fills its SMs' shared
     // memory; the split kernel, launched before that one ends, gets the others.
-    // Shares by the SM time that each was measured to take (us): a key tile there,
-    // a step here; how full the caches are only the device knows: two thirds.
-    // Measured against one after the other, each on all SMs: 37 us for 41 (32
-    // sequences behind 8192 keys, d 128); 24 x 5 rows behind 20001 keys (d 256): 124
-    // for 125, with the row tiles in step (below) 105.
-    const double tile_us = D == 64 ? 1.3 : (D == 128 ? 1.8 : 3.2), step_us = D == 64 ? 0.28 : (D == 128 ? 0.56 : 0.39);
-    const double cost_t = tile_us * lt.prefix_units * tiles(lt, p.Np);
-    const double cost_w = step_us * p.B * p.Hkv * tiles(lw, p.Ncap) * 2 / 3;
-    lt.n_ctas = std::min(kSms - 8, std::max(8, (int)(kSms * cost_t / (cost_t + cost_w) + 0.5)));
-    if (lt.prefix_rt > 1 && lt.prefix_units < kSms - 8)  // see below
-      lt.n_ctas = std::min((kSms - 8) / lt.prefix_units,
-                           std::max(1, (lt.n_ctas + lt.prefix_units / 2) / lt.prefix_units)) * lt.prefix_units;
+    // GPU time against one after the other, each on all SMs: 37 us for 41 (32
+    // sequences behind 8192 keys, d 128).
+    const CacheShare share = cache_share(lt.prefix_units, (int)tiles(lt, p.Np), lt.prefix_rt,
+                                         (long long)p.B * p.Hkv * tiles(lw, p.Ncap), D);
+    lt.n_ctas = share.n_ctas;
+    lt.split = share.split;
     lw.n_ctas = (kSms - lt.n_ctas) * W::PER_SM;
-  }
-  // Several row tiles of a prefix read the same K and V: where the same number of
-  // CTAs for every unit uses nearly all CTAs, the tiles go in step and L2 serves
-  // all but the first.
-  if (lt.prefix_rt > 1 && lt.own_rt == 0) {
+  } else if (lt.prefix_rt > 1 && lt.own_rt == 0) {
+    // the prefix alone: in step (see cache_share) where the same number of CTAs for
+    // every unit uses nearly all CTAs
     const int split = lt.n_ctas / lt.prefix_units;
     if (10 * split * lt.prefix_units >= 9 * lt.n_ctas) lt.split = split;
   }
@@ -504,6 +544,22 @@ fa_status fa_key_weights(const void* q, const void* k, const float* lse, const i
   if (st != FA_OK) return st;
   return key_weights_run(q, k, lse, lengths, weights, weights_out, B, Hq, Hkv, Nq, Nk, d, causal, scale, workspace, di->err,
                          static_cast<cudaStream_t>(stream));
+}
+
+fa_status fa_selftest_cache_share(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, int* share) {
+  bool empty = false;
+  const fa_status st = cache_sizes(B, Hq, Hkv, Nq, Np, Ncap, d, 1.f, &empty);
+  if (st != FA_OK) return st;
+  if (!share) return FA_ERR_INVALID_ARG;
+  share[0] = share[1] = 0;
+  const CachePlan pl = cache_plan(B, Hq, Hkv, Nq, Np, Ncap, d, false);
+  if (empty || pl.units_t == 0 || pl.units_w == 0) return FA_OK;
+  const int rt = (int)(((long long)B * (Hq / Hkv) * Nq + 127) / 128);
+  const int keys = d == 256 ? fa::CacheCfg<256>::CH : fa::CacheCfg<128>::CH;
+  const CacheShare s = cache_share(Hkv * rt, (Np + 127) / 128, rt, (long long)B * Hkv * ((Ncap + keys - 1) / keys), d);
+  share[0] = s.n_ctas;
+  share[1] = s.split;
+  return FA_OK;
 }
 
 fa_status fa_cache_evict(const void* k, const void* v, const float* weights, const int* lengths, void* k_out,

@@ -151,6 +151,13 @@ fa_status fa_selftest_wait_timeout(long long cap_cycles, void* stream);
  * (use_poly = 1). */
 fa_status fa_selftest_exp2(const float* x, float* y, long long n, int use_poly, void* stream);
 
+/* Self-test of a host rule, without a GPU: how fa_fwd_decode_prefix divides the
+ * SMs between its two attention kernels for these sizes.  share[0] is the number
+ * of CTAs (one an SM) for the prefix, share[1] the number for each of its units
+ * where its row tiles go in step (0: equal runs); both 0 where the two kernels do
+ * not run side by side. */
+fa_status fa_selftest_cache_share(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, int* share);
+
 /* ------------------------------------------------------------------------
  * Decoding: Nq query rows per head against Nk cached keys and values.
  *
