@@ -234,12 +234,20 @@ CachePlan cache_plan(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d, bo
     pl.t_range = take((size_t)pl.units_t * sizeof(int2));
   }
   // Few rows: their scores are kept (4 bytes a row and key, written and read once)
-  // and turned into weights by the kernel that joins the results.  More rows, or
-  // scores that L2 does not hold: the keys are read once more by the kernel for
-  // known LSE (2d bytes a key).  4 x 8 drafted tokens, 64 rows a kv head, 10007
-  // keys: 31 us with scores, 37 with the second reading.
+  // and turned into weights by the kernel that joins the results.  Otherwise the keys
+  // are read once more by the kernel for known LSE (2d bytes a key, and two launches).
+  // With scores and with the second reading (us):
+  //   up to 16 rows    205 and 307 (8 x 8 x 32768 keys, 4 rows, d 128), 248 and 307 (16
+  //                    rows), 166 and 207 (16 rows, d 64): always scores
+  //   17 to 64 rows    by what there is to store.  32 MB: d 64 47 to 80 and 45 to 78, d 128
+  //                    55 to 88 and 57 to 90, d 256 82 to 127 and 86 to 135; 48 MB: d 64 76
+  //                    and 55, d 128 78 and 68 (64 rows); 64 MB: d 256 125 and 127, 80 MB: 154
+  //                    and 141
+  //   96 rows          51 and 49 (4 x 2 x 10007 keys, 31 MB), but 25 and 31 with 2000 keys: the
+  //                    joining kernel holds the LSE of kCacheScoreRows rows
   const size_t score_bytes = (size_t)B * Hkv * R * (((size_t)Ncap + 127) / 128 * 128) * 4;
-  pl.scores = weights && (!pl.tc_o || (R <= fa::kCacheScoreRows && score_bytes <= (size_t)64 << 20));
+  const size_t most = (size_t)(d == 256 ? 64 : 32) << 20;
+  pl.scores = weights && (!pl.tc_o || (R <= fa::kCacheScoreRows && score_bytes <= most));
   pl.key_weights = weights && !pl.scores;
   if (pl.scores) pl.score_off = take(score_bytes);
   if (pl.key_weights) pl.keyw_off = take(key_weights_plan(B, Hq, Hkv, Nq, Ncap, d).total());

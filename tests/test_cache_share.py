@@ -94,3 +94,19 @@ def test_no_division_where_one_kernel_runs():
     for c in ((2, 3, 2, 1, 500, 100, 64), (2, 4, 2, 1, 500, 100, 96), (2, 4, 2, 1, -1, 100, 64)):
         with pytest.raises(FAError):
             binding.fa_selftest_cache_share(*c)
+
+
+@pytest.mark.parametrize("d,most", [(64, 32), (128, 32), (256, 64)])
+def test_scores_are_stored_only_while_they_are_few(d, most):
+    """17 to 64 query rows against a sequence's keys: more than `most` MB of scores
+    would take longer than reading the keys again, so the workspace has no room for
+    them; up to 16 rows, or no more than `most` MB, it has."""
+    def workspace(B, G, Nq, n):
+        return binding.fa_decode_weights_workspace_bytes(B, 8 * G, 8, Nq, n, d)
+
+    for B, G, Nq in ((8, 8, 8), (1, 4, 8), (2, 3, 6)):
+        row = B * 8 * G * Nq * 4  # bytes of one key's scores
+        n = (most << 20) // row // 128 * 128
+        assert workspace(B, G, Nq, n) >= n * row
+        assert workspace(B, G, Nq, n + 128) < workspace(B, G, Nq, n)
+    assert workspace(8, 16, 1, 32768) >= 8 * 8 * 16 * 32768 * 4
