@@ -548,7 +548,8 @@ def attention_key_weights(q, k, lse, weights=None, lengths=None, causal=False, s
     """The attention weight that every key of the caches k [B,Hkv,Nk,d] receives
     from the queries q [B,Hq,Nq,d] (the last Nq positions of each sequence)
     whose lse [B,Hq,Nq] is known, added to weights (fp32 [B,Hkv,Nk]; None:
-    zero); see fa_key_weights.  Returns weights_out."""
+    zero); see fa_key_weights, also for prompts of different lengths, whose rows
+    have to end with them.  Returns weights_out."""
     call = _CacheCall("attention_key_weights", q, stream)
     B, Hq, Nq, d, Hkv, Nk = call.dims(q, k)
     check = call.check

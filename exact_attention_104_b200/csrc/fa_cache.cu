@@ -318,8 +318,11 @@ fa_status launch_cache(const CUtensorMap (&maps)[4], fa::CacheParams p, fa::Cach
     // once, on SMs of their own, since one is bound by its softmax and the other
     // by reading keys.  The tcgen05 kernel goes first and fills its SMs' shared
     // memory; the split kernel, launched before that one ends, gets the others.
-    // GPU time against one after the other, each on all SMs: 37 us for 41 (32
-    // sequences behind 8192 keys, d 128).
+    // GPU time with caches full, two thirds and a tenth full, against one after the
+    // other, each on all SMs (us): 47, 47, 41 and 59, 53, 41 (32 sequences behind 8192
+    // keys, caches of 1024, d 128); 126, 109, 100 and 131, 119, 98 (24 x 5 rows behind
+    // 20001, caches of 1500, d 256); 238, 174, 64 and 260, 190, 70 (240 behind 128,
+    // caches of 1500, d 128).
     const CacheShare share = cache_share(lt.prefix_units, (int)tiles(lt, p.Np), lt.prefix_rt,
                                          (long long)p.B * p.Hkv * tiles(lw, p.Ncap), D);
     lt.n_ctas = share.n_ctas;

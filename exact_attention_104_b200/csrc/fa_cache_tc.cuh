@@ -14,12 +14,17 @@
 //
 // P goes into the second product as the sum of two bf16 numbers (high part and
 // remainder): with a weight good to 2^-16, O is as good as its own rounding.
-// That costs a third more tensor work and 6 % of the time.
+// That is half more tensor work (three products a tile for two) and cost 6 % of
+// the time.
 //
-// Measured: 8 kv heads x 8192 keys for 128 rows (d = 128), all SMs: 17 us, of
-// which four tiles a CTA take 5 and the rest are start and end; 16 units x 20001
-// keys for 240 rows (d = 256): 82 us, 3.2 us a tile.  There the ring bounds it:
-// 160 KB hold little more than one tile's K and V, so their latency shows.
+// Measured (K and V from HBM): 8 kv heads x 8192 keys for 128 rows (d = 128), all
+// SMs: 22 us, of which four tiles a CTA take 7 and the rest are start and end; 16
+// units x 20001 keys for 240 rows (d = 256), the two row tiles in step: 73 us, 3.2 us a
+// tile, the prefix read from HBM once.  Two things are known to stretch a tile there.
+// The ring: 160 KB hold little more than one tile's K and V, so their latency shows.
+// And registers: 384 threads have 168 each, and the softmax loop's 64 scores and 64
+// words of P do not fit, so 324, 316 and 364 bytes a thread (d = 64, 128, 256) are
+// spilled.  How much each costs has not been measured.
 //
 // The two warps of 32 rows meet at named barriers.  A warp whose wait gave up
 // therefore goes on through the same barriers, without doing anything else.

@@ -18,8 +18,13 @@
 // of up to 8192 weights is read once and stays in registers; larger ones are
 // read four times.
 //
-// Measured, 4 x 8 x 65536 weights cut to 8192 (d = 128): selection 23 us, most of
-// it the cluster's barriers; copy 43 us, 6.4 TB/s of kept rows read and written.
+// Measured, 4 x 8 x 65536 weights cut to 8192 (d = 128): copy 43 us, 6.4 TB/s of kept
+// rows read and written; selection 21 to 30 us.  Of that, 13 us are what a CTA does
+// with its 8192 weights (16 x 8 x 8192, no cluster: 13 to 14 us, whether they are all
+// equal or spread evenly over the bins, so it is not the atomic additions that
+// bound it; 40 % of the issue slots are used), and the rest are the cluster's
+// barriers and the bins sent: 21 us where all weights are equal, 22 where they
+// spread over a few powers of two, 27 over all, 30 where they are uniform in 0 .. 1.
 #pragma once
 
 #include "sm100.cuh"

@@ -35,12 +35,13 @@
 //   warps 4-19    four warpgroups, a 128-key part of a step each in turn;
 //                 thread = key
 //
-// Measured (B200, 8192-token prompt, 16 heads on 4 kv heads, d = 128): 169 us.
-// The exponentials alone would take 123 us at 1.9 GHz, the product 85 us at
-// 1.63 PFLOP/s; a warpgroup computes 70 % of the time and waits for its next
+// Measured (B200, 8192-token prompt, 16 heads on 4 kv heads, d = 128): 176 us a call
+// on the GPU, 190 one call after the other from Python.  The three quarters of the
+// exponentials that the special-function unit takes would last 92 us at 1.9 GHz, the
+// product 85 us at 1.63 PFLOP/s; a warpgroup computes 70 % of the time and waits for its next
 // product in most of the rest, since 512 TMEM columns hold one S buffer for
-// each of the four warpgroups and no more.  Three warpgroups with a buffer to
-// spare: 181 us.
+// each of the four warpgroups and no more.  (Three warpgroups with a buffer to
+// spare took 181 us where four took 169.)
 #pragma once
 
 #include "sm100.cuh"

@@ -260,10 +260,10 @@ fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, const void*
  * Decoding for a batch that shares a prefix: sequence b is the Np keys of the
  * prefix (k_prefix, v_prefix: bf16 [Hkv, Np, d], one copy for the batch)
  * followed by its own lengths[b] keys out of k, v [B, Hkv, Ncap, d], so
- * L = Np + lengths[b].  The prefix is read once for each tile of the B * Hq/Hkv * Nq
- * query rows of a kv head (16 or 128 rows), not once for each sequence.  Np == 0 (k_prefix, v_prefix may be NULL) is decoding
- * over ragged caches; Ncap == 0 (k, v may be NULL) decoding over the prefix
- * alone.  q, o bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] (natural log);
+ * L = Np + lengths[b].  The prefix is read once for each tile of the
+ * B * Hq/Hkv * Nq query rows of a kv head (16 or 128 rows), not once for each
+ * sequence.  Np == 0 (k_prefix, v_prefix may be NULL) is decoding over ragged
+ * caches; Ncap == 0 (k, v may be NULL) decoding over the prefix alone.  q, o bf16 [B, Hq, Nq, d], lse fp32 [B, Hq, Nq] (natural log);
  * Nq <= 256.  The softmax is put together from the key runs' partial results
  * as in fa_fwd_decode. */
 size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ncap, int d);
@@ -285,11 +285,14 @@ fa_status fa_fwd_decode_weights(const void* q, const void* k, const void* v, con
                                 int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The same weights from queries whose LSE is known: those of a prompt after
- * fa_fwd (Nq == Nk == N), or of its last Nq positions.  Any Nq >= 0.  lse fp32 [B, Hq, Nq], natural log, as fa_fwd
- * writes it for the same q, k, causal and scale.  In a padded batch, query rows
- * end with the sequence as everywhere here: row i of sequence b is position
+ * fa_fwd (Nq == Nk == N), or of its last Nq positions.  Any Nq >= 0.  lse fp32
+ * [B, Hq, Nq], natural log, as fa_fwd writes it for the same q, k, causal and
+ * scale (with another LSE the weights are undefined).  In a padded batch, query
+ * rows end with the sequence as everywhere here: row i of sequence b is position
  * lengths[b] - Nq + i, and rows whose position is negative give no weight when
- * causal (whatever their q and lse hold). */
+ * causal (whatever their q and lse hold).  A forward pass over a right-padded
+ * batch leaves row i at position i: for prompts of different lengths, move rows
+ * 0 .. lengths[b] - 1 of q and lse to Nq - lengths[b] .. Nq - 1 first. */
 size_t fa_key_weights_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 fa_status fa_key_weights(const void* q, const void* k, const float* lse, const int* lengths, const float* weights,
                          float* weights_out, int B, int Hq, int Hkv, int Nq, int Nk, int d, int causal, float scale,
