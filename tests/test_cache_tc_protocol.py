@@ -42,7 +42,7 @@ def _simulate(runs, nslot, nch, seed, mistake=None):
     wait, wait_named = _waiter(bars), _waiter(named)
     tma, pipe = [], []
     slot = [None] * nslot
-    scores, score_run = [None, None], {}         # tile whose scores or weights a buffer holds
+    scores = [None, None]                        # tile whose scores or weights a buffer holds
     read, weights = {}, {}                       # warps that have read a tile's scores, written its weights
     q_tile, staging = {w: None for w in WARPS}, set()  # run whose Q each warp wrote; warps whose O is staged
     s_done, pv_done = set(), set()
